@@ -41,7 +41,9 @@ EXPORTED = ("llama_model_bytes", "llama_model_create", "llama_set_weight", "llam
             "llama_op_rmsnorm", "llama_op_linear", "llama_op_linear_workspace_bytes", "llama_op_linear_noalloc",
             "llama_profile_start", "llama_profile_stop", "llama_token_logprobs", "llama_timeline_start",
             "llama_timeline_stop", "llama_debug_stall", "llama_model_bytes_tp", "llama_model_create_tp",
-            "llama_tp_prefill_all", "llama_tp_decode_step_all", "llama_tp_buffers", "llama_tp_bind")
+            "llama_tp_prefill_all", "llama_tp_decode_step_all", "llama_tp_buffers", "llama_tp_bind",
+            "llama_paged_plan", "llama_rope_table", "llama_paged_append", "llama_paged_attention_workspace_bytes",
+            "llama_paged_attention", "llama_sample_rows")
 LLAMA_STALL_NONE, LLAMA_STALL_PROJECTION, LLAMA_STALL_ATTENTION = 0, 1, 2
 TIMELINE_KINDS = {0: "embed", 1: "projection", 2: "attention", 3: "sample", 4: "rmsnorm"}
 
@@ -115,6 +117,15 @@ _sig("llama_profile_start", _i, [_vp, _i])
 _sig("llama_profile_stop", _i, [_vp, ctypes.POINTER(ctypes.c_float), ctypes.POINTER(ctypes.c_int64),
                                 ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int32), _i,
                                 ctypes.POINTER(ctypes.c_int)])
+_i64 = ctypes.c_int64
+_sig("llama_paged_plan", _i, [_vp, _vp, _i, _i, _vp, _i, _vp, _i, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp])
+_sig("llama_rope_table", _i, [_vp, _i, _i, _f, _vp])
+_sig("llama_paged_append", _i, [_vp, _i64, _vp, _i64, _vp, _i64, _i, _i, _i, _i, _i, _vp, _vp, _f, _vp, _i, _vp, _vp,
+                                _vp, _vp, _vp, _i, _i, _i, _vp, _vp])
+_sig("llama_paged_attention_workspace_bytes", _sz, [_i, _i, _i, _i, _i])
+_sig("llama_paged_attention", _i, [_vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _i, _i, _i, _i, _f, _vp, _vp,
+                                   _sz, _vp, _vp])
+_sig("llama_sample_rows", _i, [_vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp])
 
 
 def lib():
@@ -585,4 +596,185 @@ def op_linear(A, W, out, stream=None, workspace=None):
     ws = workspace if workspace is not None else (op_linear_workspace(A.device) if dt != LLAMA_F32 else None)
     _check(_lib.llama_op_linear(A.data_ptr(), W.data_ptr(), M, N, K, dt, out.data_ptr(), _ptr(ws),
                                 0 if ws is None else ws.numel(), _stream(stream)))
+    return out
+
+
+# ---------------------------------------------------------------- a serving step over a paged KV cache
+
+def _arg(t, dtype: str, shape, name: str, device):
+    """A contiguous tensor of torch dtype `dtype` and shape `shape` on `device` (None in `shape`: any size)."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if str(t.dtype) != "torch." + dtype:
+        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _home(t, name: str):
+    """The device of a call's first tensor, which must be the current CUDA device (the stream's)."""
+    import torch
+    if not getattr(t, "is_cuda", False):
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t.device
+
+
+def _status_arg(status, device):
+    if status is not None:
+        _arg(status, "int32", (1,), "status", device)
+
+
+def paged_plan(ctx_lens, new_lens, block_tables, free_pages, free_count, page_size: int, seq_lens, cu_new, slots,
+               positions, free_left, status=None, stream=None):
+    """Block tables, slots, positions and offsets of one serving step from its
+    lengths (llama_paged_plan).  int32 tensors: ctx_lens, new_lens, seq_lens
+    [B], block_tables [B, max_pages] (new pages are added in place),
+    free_pages [n_pages] and free_count [1] (the stack of free pages),
+    cu_new [B+1], positions [T], free_left [1]; int64 slots [T].  seq_lens may
+    be ctx_lens and free_left may be free_count: the step then updates them."""
+    dev = _home(ctx_lens, "ctx_lens")
+    B, T = ctx_lens.numel(), slots.numel()
+    _arg(ctx_lens, "int32", (B,), "ctx_lens", dev)
+    _arg(new_lens, "int32", (B,), "new_lens", dev)
+    _arg(block_tables, "int32", (B, None), "block_tables", dev)
+    _arg(free_pages, "int32", (None,), "free_pages", dev)
+    _arg(free_count, "int32", (1,), "free_count", dev)
+    _arg(seq_lens, "int32", (B,), "seq_lens", dev)
+    _arg(cu_new, "int32", (B + 1,), "cu_new", dev)
+    _arg(slots, "int64", (T,), "slots", dev)
+    _arg(positions, "int32", (T,), "positions", dev)
+    _arg(free_left, "int32", (1,), "free_left", dev)
+    _status_arg(status, dev)
+    _check(_lib.llama_paged_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), B, page_size, block_tables.data_ptr(),
+                                 block_tables.shape[1], free_pages.data_ptr(), free_pages.numel(),
+                                 free_count.data_ptr(), T, seq_lens.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
+                                 positions.data_ptr(), free_left.data_ptr(), _ptr(status), _stream(stream)))
+
+
+def rope_table(out, theta: float = 10000.0, stream=None):
+    """Fills out, fp32 [len, head_dim/2, 2], with the rotation table that paged_append reads."""
+    dev = _home(out, "out")
+    _arg(out, "float32", (None, None, 2), "out", dev)
+    _check(_lib.llama_rope_table(out.data_ptr(), out.shape[0], 2 * out.shape[1], float(theta), _stream(stream)))
+    return out
+
+
+def _rows(t, name: str, T: int, hd: int, device):
+    """A [T, heads, head_dim] view whose heads are contiguous; returns its row stride in elements."""
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != hd:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({T}, heads, {hd})")
+    row = t.shape[1] * hd
+    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != hd):
+        raise ValueError(f"{name} must have contiguous heads")
+    return t.stride(0) if T > 1 else row
+
+
+def _pools(k_pages, v_pages, dtype: str, device):
+    """(n_pages, n_kv_heads, page_size, head_dim) of a K and a V pool."""
+    _arg(k_pages, dtype, (None,) * 4, "k_pages", device)
+    _arg(v_pages, dtype, tuple(k_pages.shape), "v_pages", device)
+    return k_pages.shape
+
+
+def paged_append(q, k, v, positions, slots, rope, q_out, k_pages, v_pages, q_norm=None, k_norm=None,
+                 eps: float = 1e-5, status=None, stream=None):
+    """Per-head RMSNorm of q and k (q_norm, k_norm fp32 [head_dim]; None: no
+    norm), rotation by `positions` (rope: rope_table), rotated q to q_out
+    [T, n_heads, head_dim], K and V to their `slots` of k_pages / v_pages
+    [n_pages, n_kv_heads, page_size, head_dim] (llama_paged_append).  q, k, v
+    are [T, heads, head_dim] views with any row stride, float32 or of the
+    cache's dtype."""
+    dev = _home(q, "q")
+    code = _dtype_code(q_out, "q_out")
+    dt = str(q_out.dtype)[6:]
+    n_pages, nkv, page, hd = _pools(k_pages, v_pages, dt, dev)
+    T, nh = q.shape[0], q.shape[1]
+    sq, sk, sv = _rows(q, "q", T, hd, dev), _rows(k, "k", T, hd, dev), _rows(v, "v", T, hd, dev)
+    _need(k.shape[1] == nkv and v.shape[1] == nkv, "k and v must have the pool's heads")
+    _need(k.dtype == q.dtype and v.dtype == q.dtype, "q, k and v must have one dtype")
+    in_code = _dtype_code(q, "q")
+    _arg(q_out, dt, (T, nh, hd), "q_out", dev)
+    _arg(rope, "float32", (None, hd // 2, 2), "rope", dev)
+    _arg(positions, "int32", (None,), "positions", dev)
+    _arg(slots, "int64", (None,), "slots", dev)
+    _need(positions.numel() >= T and slots.numel() >= T, "positions and slots need an entry per row")
+    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
+        if w is not None:
+            _arg(w, "float32", (hd,), name, dev)
+    _status_arg(status, dev)
+    _check(_lib.llama_paged_append(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, in_code, T, nh, nkv, hd,
+                                   _ptr(q_norm), _ptr(k_norm), float(eps), rope.data_ptr(), rope.shape[0],
+                                   positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
+                                   v_pages.data_ptr(), n_pages, page, code, _ptr(status), _stream(stream)))
+    return q_out
+
+
+def paged_attention_workspace(q, n_kv_heads: int, max_new: int):
+    """A zero-filled workspace for paged_attention calls on queries like q
+    ([T, n_heads, head_dim]) with at most max_new new tokens per request.
+    Calls that share one must not overlap on the device."""
+    import torch
+    n = int(_lib.llama_paged_attention_workspace_bytes(q.shape[1], n_kv_heads, q.shape[2], _dtype_code(q, "q"),
+                                                       max_new))
+    if n == 0:
+        raise LlamaError(LLAMA_ERR_INVALID_ARG, last_error())
+    return torch.zeros(n, dtype=torch.uint8, device=q.device)
+
+
+def paged_attention(q, k_pages, v_pages, block_tables, cu_new, seq_lens, out, max_new: Optional[int] = None,
+                    scale: Optional[float] = None, workspace=None, status=None, stream=None):
+    """Causal attention of each request's new tokens (packed rows cu_new[b] ..
+    of q [T, n_heads, head_dim]) over its pages (llama_paged_attention).
+    max_new: most new tokens of one request (None: T); scale: 1/sqrt(head_dim)
+    if None.  workspace: paged_attention_workspace(), kept by the caller; None
+    makes a new one for this call."""
+    dev = _home(q, "q")
+    code = _dtype_code(q, "q")
+    dt = str(q.dtype)[6:]
+    n_pages, nkv, page, hd = _pools(k_pages, v_pages, dt, dev)
+    T, nh = q.shape[0], q.shape[1]
+    _arg(q, dt, (T, nh, hd), "q", dev)
+    _arg(out, dt, (T, nh, hd), "out", dev)
+    B = seq_lens.numel()
+    _arg(seq_lens, "int32", (B,), "seq_lens", dev)
+    _arg(cu_new, "int32", (B + 1,), "cu_new", dev)
+    _arg(block_tables, "int32", (B, None), "block_tables", dev)
+    _status_arg(status, dev)
+    if max_new is None:
+        max_new = max(T, 1)
+    if workspace is None:
+        import torch
+        with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
+            workspace = paged_attention_workspace(q, nkv, max_new)
+    else:
+        _arg(workspace, "uint8", (None,), "workspace", dev)
+    _check(_lib.llama_paged_attention(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), code, T, nh, nkv, hd, B,
+                                      cu_new.data_ptr(), seq_lens.data_ptr(), block_tables.data_ptr(),
+                                      block_tables.shape[1], n_pages, page, int(max_new),
+                                      float(scale) if scale is not None else hd ** -0.5, out.data_ptr(),
+                                      workspace.data_ptr(), workspace.numel(), _ptr(status), _stream(stream)))
+    return out
+
+
+def sample_rows(logits, temperature, uniforms, out, top_k=None, top_p=None, min_p=None, stream=None):
+    """Next tokens with each row's own parameters (llama_sample_rows): fp32
+    logits [B, V]; temperature, uniforms, top_p, min_p fp32 [B], top_k int32
+    [B] (None: that filter is off); out int32 [B]."""
+    dev = _home(logits, "logits")
+    _arg(logits, "float32", (None, None), "logits", dev)
+    B, V = logits.shape
+    _arg(temperature, "float32", (B,), "temperature", dev)
+    _arg(uniforms, "float32", (B,), "uniforms", dev)
+    _arg(out, "int32", (B,), "out", dev)
+    for t, dt, name in ((top_k, "int32", "top_k"), (top_p, "float32", "top_p"), (min_p, "float32", "min_p")):
+        if t is not None:
+            _arg(t, dt, (B,), name, dev)
+    _check(_lib.llama_sample_rows(logits.data_ptr(), B, V, temperature.data_ptr(), _ptr(top_k), _ptr(top_p),
+                                  _ptr(min_p), uniforms.data_ptr(), out.data_ptr(), _stream(stream)))
     return out

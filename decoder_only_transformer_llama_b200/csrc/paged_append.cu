@@ -1,0 +1,142 @@
+// Per-head RMSNorm of queries and keys, rotation by position, and the write
+// of K and V into their cache slots, in one pass over a step's projections
+// (Admin Guide §8.4: RMSNorm, apply_rotary_emb, Attention step 4).
+//
+//   y = x / sqrt(mean(x^2) + eps) * w          per head; without weights y = x
+//   (y[2j], y[2j+1]) -> (y[2j] c - y[2j+1] s, y[2j] s + y[2j+1] c),  (c, s) = rope[position][j]
+//
+// in fp32, rounded once to the cache's type.  Bound by HBM: every value is
+// read once and written once.  A lane holds 16 bytes of one head; the
+// HD * sizeof(input) / 16 lanes of a head sum its squares by shuffles.
+#include <type_traits>
+
+#include "common.cuh"
+#include "paged.h"
+
+namespace llb {
+
+namespace {
+constexpr int kThreads = 256;
+
+template <typename TI, int N>
+__device__ __forceinline__ void load_vec(const TI* p, float (&v)[N]) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const TI* h = reinterpret_cast<const TI*>(&u);
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] = to_f32<TI>(h[i]);
+}
+
+template <typename TO, int N>
+__device__ __forceinline__ void store_vec(TO* p, const float (&v)[N]) {
+    if constexpr (sizeof(TO) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) *reinterpret_cast<float4*>(p + i) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+    } else if constexpr (N == 8) {
+        uint4 u;
+        u.x = pack2<TO>(v[0], v[1]); u.y = pack2<TO>(v[2], v[3]);
+        u.z = pack2<TO>(v[4], v[5]); u.w = pack2<TO>(v[6], v[7]);
+        *reinterpret_cast<uint4*>(p) = u;
+    } else {
+        uint2 u;
+        u.x = pack2<TO>(v[0], v[1]); u.y = pack2<TO>(v[2], v[3]);
+        *reinterpret_cast<uint2*>(p) = u;
+    }
+}
+}  // namespace
+
+template <typename TI, typename TO, int HD>
+__global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
+    constexpr int N = 16 / static_cast<int>(sizeof(TI));   // values per lane
+    constexpr int LPH = HD / N;                            // lanes per head
+    constexpr int GROUPS = kThreads / LPH;
+    const int t = blockIdx.x;
+    const long long slot = a.slots[t];
+    if (slot < 0) return;                                  // padding: nothing is written
+    const int pos = a.positions[t];
+    if (slot >= a.n_slots || pos < 0 || pos >= a.rope_len) {
+        if (threadIdx.x == 0) report_status(a.status, LLAMA_ERR_CAPACITY);
+        return;
+    }
+    const int sub = threadIdx.x % LPH;
+    const long long page = slot >> a.page_shift;
+    const long long off = slot & ((1LL << a.page_shift) - 1);
+    float cs[N], sn[N];
+    {
+        const float2* r = a.rope + static_cast<long long>(pos) * (HD / 2) + sub * (N / 2);
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) { const float2 f = r[i]; cs[i] = f.x; sn[i] = f.y; }
+    }
+    const int heads = a.nh + 2 * a.nkv;
+    for (int h0 = blockIdx.y * GROUPS; h0 < heads; h0 += gridDim.y * GROUPS) {
+        const int h = h0 + threadIdx.x / LPH;
+        const bool live = h < heads;
+        const bool is_q = h < a.nh, is_k = !is_q && h < a.nh + a.nkv;
+        const TI* src = is_q ? static_cast<const TI*>(a.q) + t * a.q_stride + h * HD
+                      : is_k ? static_cast<const TI*>(a.k) + t * a.k_stride + (h - a.nh) * HD
+                             : static_cast<const TI*>(a.v) + t * a.v_stride + (h - a.nh - a.nkv) * HD;
+        float x[N];
+        if (live) load_vec<TI, N>(src + sub * N, x);
+        else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) x[i] = 0.f;
+        }
+        const float* w = is_q ? a.q_norm : is_k ? a.k_norm : nullptr;
+        if (a.q_norm || a.k_norm) {                        // the same for every thread: shuffles stay warp-wide
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+            for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            if (w) {
+                const float inv = 1.f / sqrtf(ss / HD + a.eps);
+#pragma unroll
+                for (int i = 0; i < N; ++i) x[i] = x[i] * inv * w[sub * N + i];
+            }
+        }
+        if (!live) continue;
+        TO* dst;
+        if (is_q) dst = static_cast<TO*>(a.q_out) + (static_cast<long long>(t) * a.nh + h) * HD;
+        else {
+            const int g = is_k ? h - a.nh : h - a.nh - a.nkv;
+            dst = static_cast<TO*>(is_k ? a.k_pages : a.v_pages) +
+                  (((page * a.nkv + g) << a.page_shift) + off) * HD;
+        }
+        if (is_q || is_k) {
+            float y[N];
+#pragma unroll
+            for (int i = 0; i < N / 2; ++i) {
+                y[2 * i] = x[2 * i] * cs[i] - x[2 * i + 1] * sn[i];
+                y[2 * i + 1] = x[2 * i] * sn[i] + x[2 * i + 1] * cs[i];
+            }
+            store_vec<TO, N>(dst + sub * N, y);
+        } else {
+            store_vec<TO, N>(dst + sub * N, x);
+        }
+    }
+}
+
+template <typename TI, typename TO, int HD>
+static int append_go(const AppendArgs& a, cudaStream_t st) {
+    paged_append_kernel<TI, TO, HD><<<dim3(a.T, 1), kThreads, 0, st>>>(a);
+    LLB_CHECK_LAUNCH("paged_append_kernel");
+    return LLAMA_OK;
+}
+
+template <typename TI, typename TO>
+static int append_hd(const AppendArgs& a, cudaStream_t st) {
+    switch (a.hd) {
+        case 32: return append_go<TI, TO, 32>(a, st);
+        case 64: return append_go<TI, TO, 64>(a, st);
+        default: return append_go<TI, TO, 128>(a, st);
+    }
+}
+
+int launch_paged_append(const AppendArgs& a, int in_dtype, int dtype, cudaStream_t st) {
+    if (in_dtype == LLAMA_BF16) return append_hd<bf16, bf16>(a, st);
+    if (in_dtype == LLAMA_F16) return append_hd<f16, f16>(a, st);
+    if (dtype == LLAMA_BF16) return append_hd<float, bf16>(a, st);
+    if (dtype == LLAMA_F16) return append_hd<float, f16>(a, st);
+    return append_hd<float, float>(a, st);
+}
+
+}  // namespace llb

@@ -202,6 +202,31 @@ LLAMA_API int llama_decode_step(llama_model* m, const int32_t* tokens, int32_t* 
 LLAMA_API int llama_sample(const float* logits, int B, int V, float temperature, float top_p,
                  const float* uniforms, int32_t* out, void* stream);
 
+/* Sampling with parameters of their own for each row (a batch of requests):
+ *   logits       device fp32 [B, V], V <= 262144
+ *   temperature  device fp32 [B]; 0 selects the greedy argmax of that row
+ *   top_k        device int32 [B] or NULL; values <= 0 or >= V keep every token
+ *   top_p        device fp32 [B] or NULL; values >= 1 keep every token
+ *   min_p        device fp32 [B] or NULL, in [0, 1]; 0 keeps every token
+ *   uniforms     device fp32 [B] in [0, 1) (clamped to it; read for every row)
+ *   out          device int32 [B]
+ * In fp64: e = exp((logit - max logit) / temperature); tokens ordered by logit
+ * descending, ties by id ascending.  Kept are the first top_k tokens; of them
+ * those whose mass before them is <= top_p * (mass of the first top_k); of
+ * those the ones with e >= min_p (the first token is always kept).  Returns
+ * the first token whose cumulative mass exceeds uniforms[b] * (kept mass).
+ * A NaN logit counts as -inf and a token at -inf is never drawn; if the
+ * largest logit is +inf, the tokens at +inf share the mass equally.  A row
+ * without any logit above -inf gives token 0.  A row whose temperature is
+ * negative, NaN or infinite, whose top_p is negative or NaN, or whose min_p
+ * is outside [0, 1] or NaN gives -1.  With top_k and min_p off and V tokens
+ * of distinct mass the picks are those of llama_sample.  Needs no model and
+ * no workspace.  LLAMA_ERR_INVALID_ARG for NULL pointers and sizes out of
+ * range; B == 0 is a no-op. */
+LLAMA_API int llama_sample_rows(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
+                                const float* top_p, const float* min_p, const float* uniforms, int32_t* out,
+                                void* stream);
+
 /* Log-probabilities of given tokens under their logits rows: the per-token
  * logprobs that the generation loop returns (Admin Guide §8.5, generate with
  * logprobs=True):

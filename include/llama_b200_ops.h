@@ -3,7 +3,8 @@
  *
  * Each call runs one of the kernels the model path uses, on caller device
  * buffers, so that a kernel can be checked against the CPU oracle on its own
- * and timed in isolation.  Conventions (device pointers, void* stream,
+ * and timed in isolation, or an operator of a serving step over a paged KV
+ * cache (llama_paged_*).  Conventions (device pointers, void* stream,
  * LLAMA_OK / LLAMA_ERR_* return codes, llama_last_error) are those of
  * llama_b200.h.
  */
@@ -69,6 +70,100 @@ LLAMA_API int llama_op_linear(const void* A, const void* W, int M, int N, int K,
  *   streams, or threads without ordering) race and give wrong results. */
 LLAMA_API int llama_op_linear_noalloc(const void* A, const void* W, int M, int N, int K, float* out,
                                       void* stream);
+
+/* ---- a serving step over a paged KV cache -----------------------------------
+ * The model's cache holds max_batch_size rows of max_seq_len positions
+ * (llama_get_kv).  These operators serve requests of any mix of lengths from
+ * a caller-owned pool of pages instead; one step runs
+ *   llama_paged_plan -> llama_paged_append -> llama_paged_attention
+ * (append and attention once per layer, on that layer's pools), and
+ * llama_sample_rows draws the next tokens.  Shapes shared by the calls:
+ *   pools         k_pages, v_pages [n_pages, n_kv_heads, page_size, head_dim] in
+ *                 the cache's dtype; page_size 16, 32, 64, 128 or 256
+ *   block_tables  int32 [B, max_pages]: entry i of row b is the page that holds
+ *                 positions i*page_size .. of request b
+ *   slot          page * page_size + position % page_size: a position's place in a pool
+ *   packed rows   the new tokens of request b are rows cu_new[b] .. cu_new[b+1]-1
+ * head_dim is 32, 64 or 128, n_heads / n_kv_heads 1, 2, 4 or 8, B at most 1024.
+ * All lengths live in device memory: a step can be captured in a CUDA graph
+ * and replayed.  `status` is a caller-owned device int32 (or NULL) that keeps
+ * the first error code a kernel reports; the caller clears it. */
+
+/* Block tables, slots, positions and offsets of one step, from its lengths.
+ *   ctx_lens    int32 [B]: tokens of each request already in the cache
+ *   new_lens    int32 [B]: tokens each request adds (0 allowed); negative: the
+ *               request has ended and its ceil(ctx/page_size) pages go back to the list
+ *   free_pages  int32 [n_pages]: a stack of free page ids, *free_count of them
+ * Pages of ended requests are pushed in request order, then every growing
+ * request takes ceil((ctx+new)/page_size) - ceil(ctx/page_size) pages from
+ * the top, in request order, appended to its row of block_tables; the row of
+ * an ended request and entries behind a request's pages are left as they were.
+ *   seq_lens    int32 [B] out: ctx + new, 0 for an ended request (may be ctx_lens itself)
+ *   cu_new      int32 [B+1] out: packed rows before each request, total at the end
+ *   slots       int64 [T] out, positions int32 [T] out: of every packed row; -1
+ *               behind the last row.  T is the arrays' length, at least the step's total
+ *   free_left   int32 [1] out: free pages after the step (may be free_count itself)
+ * All or nothing: if the step needs more pages than are free, more than
+ * max_pages per request or more than T rows (LLAMA_ERR_CAPACITY in status), or a
+ * ctx or free_count is negative or more pages are free than n_pages
+ * (LLAMA_ERR_INVALID_ARG), nothing is taken or returned: every request adds no
+ * token (cu_new all 0, slots and positions -1) and seq_lens and free_left repeat
+ * their inputs.  Other outputs must not overlap inputs. */
+LLAMA_API int llama_paged_plan(const int32_t* ctx_lens, const int32_t* new_lens, int B, int page_size,
+                               int32_t* block_tables, int max_pages, int32_t* free_pages, int n_pages,
+                               const int32_t* free_count, int T, int32_t* seq_lens, int32_t* cu_new, int64_t* slots,
+                               int32_t* positions, int32_t* free_left, int32_t* status, void* stream);
+
+/* The rotation table llama_paged_append reads: rope fp32 [len, head_dim/2, 2] =
+ * (cos, sin)(t * theta^(-2j/head_dim)), in fp64 rounded once (Admin Guide §8.4). */
+LLAMA_API int llama_rope_table(float* rope, int len, int head_dim, float theta, void* stream);
+
+/* Per-head RMSNorm of queries and keys, rotation by position (adjacent pairs,
+ * Admin Guide §8.4) and the write of K and V into their slots, in one pass.
+ *   q, k, v     T rows of n_heads (n_kv_heads) * head_dim values, q_stride ...
+ *               elements apart (three views of one fused projection, say), of
+ *               in_dtype: LLAMA_F32 or the cache's dtype
+ *   q_norm, k_norm  fp32 [head_dim] or NULL (no norm)
+ *   rope        fp32 [rope_len, head_dim/2, 2];  positions int32 [T];  slots int64 [T]
+ *   q_out       [T, n_heads, head_dim] in the cache's dtype (may be q itself if
+ *               that has this type and layout); K and V go to k_pages, v_pages
+ * fp32 arithmetic, one rounding; v of the cache's dtype is copied.  A row with
+ * slot < 0 is padding: nothing of it is read or written.  A row with a slot
+ * outside the pool or a position outside the table writes nothing and sets
+ * LLAMA_ERR_CAPACITY in status.  The slots of one call must differ.  Bases,
+ * rows, rope and norm weights 16-byte aligned. */
+LLAMA_API int llama_paged_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                                 int64_t v_stride, int in_dtype, int T, int n_heads, int n_kv_heads, int head_dim,
+                                 const float* q_norm, const float* k_norm, float eps, const float* rope, int rope_len,
+                                 const int32_t* positions, const int64_t* slots, void* q_out, void* k_pages,
+                                 void* v_pages, int n_pages, int page_size, int dtype, int32_t* status, void* stream);
+
+/* Causal grouped-query attention of each request's new tokens over its pages.
+ *   q, out      [T, n_heads, head_dim] in the cache's dtype (fp32 sums)
+ *   seq_lens    int32 [B]: tokens of each request in the cache, the new ones
+ *               included: row i of request b's n new tokens sits at position
+ *               seq_lens[b] - n + i and sees keys 0 .. that position
+ *   max_new     most new tokens of one request (host): it chooses the kernel
+ *               and sizes the workspace; a request with more is still right
+ *   scale       factor of the scores (1/sqrt(head_dim) for the model's attention)
+ *   workspace   llama_paged_attention_workspace_bytes() of device scratch,
+ *               256-byte aligned, zero-filled before its first use (the kernels
+ *               leave their counters at zero); calls sharing one must not
+ *               overlap on the device.  A workspace for one max_new serves smaller ones.
+ * A row that sees no key (seq_lens[b] < n) gives zeros; rows behind the last
+ * request are left as they were.  Keys behind a request's last token and keys
+ * a row may not see do not reach its output, whatever their slots hold (NaN
+ * included).  A request with rows outside 0..T is skipped
+ * (LLAMA_ERR_INVALID_ARG in status); seq_lens[b] is cut to 0 ..
+ * max_pages*page_size (LLAMA_ERR_CAPACITY); keys of a page outside the pool read
+ * as zeros (LLAMA_ERR_INVALID_ARG). */
+LLAMA_API size_t llama_paged_attention_workspace_bytes(int n_heads, int n_kv_heads, int head_dim, int dtype,
+                                                       int max_new);
+LLAMA_API int llama_paged_attention(const void* q, const void* k_pages, const void* v_pages, int dtype, int T,
+                                    int n_heads, int n_kv_heads, int head_dim, int B, const int32_t* cu_new,
+                                    const int32_t* seq_lens, const int32_t* block_tables, int max_pages, int n_pages,
+                                    int page_size, int max_new, float scale, void* out, void* workspace,
+                                    size_t workspace_bytes, int32_t* status, void* stream);
 
 /* Per-launch timing of a model's projection kernels (for benchmarks).
  * llama_profile_start: from now on every projection launch the model enqueues
