@@ -1,84 +1,561 @@
 // Causal attention of each request's new tokens over its pages (Admin Guide
 // §8.4, Attention steps 5-7 and the mask NOTE; repeat_kv from the source tour):
-//   o = softmax_j(q . K[j] * scale) V[j],  keys j = 0 .. position of the token.
+//   o = softmax_j(q . K[j] * scale) V[j],  keys j = 0 .. position of the token,
+// in one pass over the keys with the running maximum m and sum l of the
+// softmax (o, l rescaled by 2^(m - m') when m moves, scores in the log2 domain).
 //
-// One warp per (token, head): a lane holds HD / 32 dims; online softmax.
+// A tile is 16 query rows that share one KV head (16 * n_kv_heads / n_heads
+// tokens with their query heads), a unit 32 KB of K and V.  Short steps are
+// bound by reading the cache: the units of all tiles form one list, and every
+// CTA takes an equal run of it (paged_work.cuh), so each reads the same bytes
+// whatever the mix of lengths.  Units arrive by 16-byte asynchronous copies
+// with zero fill (each row's page is looked up one unit ahead; rows behind the
+// request's last key and pages outside the pool read as zeros) in a ring of
+// three.
+//
+// 16-bit caches: warp w takes keys 16 w .. 16 w + 15 of a unit for all 16 rows,
+// S = Q K^T and O += P V as mma.sync m16n8k16 fragments (a tile of 16 rows is
+// far below tcgen05's 128; longer chunks take the kernel of
+// paged_attention_tile.cu); the warps' states are merged at the end of a tile.
+// fp32 caches: CUDA-core products (no TF32), a thread holding a 2 x 2 block of
+// scores and 16 HD / 128 outputs.
+//
+// A tile split between CTAs: each publishes its unnormalised (o, m, l) and
+// counts itself; the last to arrive merges all of them in CTA order (the same
+// bits from run to run; nobody waits) and clears the counter.
+#include <type_traits>
+
 #include "common.cuh"
 #include "paged.h"
+#include "paged_work.cuh"
 
 namespace llb {
 
-template <typename T, int HD>
-__global__ void __launch_bounds__(128) paged_attn_kernel(PagedAttnArgs a) {
-    constexpr int E = HD / 32;
-    const int lane = threadIdx.x & 31;
-    if (blockIdx.x == 0)
-        for (int b = threadIdx.x; b < a.B; b += 128)
-            if (a.cu_new[b] < 0 || a.cu_new[b + 1] < a.cu_new[b] || a.cu_new[b + 1] > a.T)
-                report_status(a.status, LLAMA_ERR_INVALID_ARG);
-    const long long item = static_cast<long long>(blockIdx.x) * 4 + (threadIdx.x >> 5);
-    if (item >= static_cast<long long>(a.T) * a.nh) return;
-    const int t = static_cast<int>(item / a.nh), h = static_cast<int>(item % a.nh);
-    int lo = 0, hi = a.B - 1;                       // the request that holds row t
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (a.cu_new[mid] <= t) lo = mid; else hi = mid - 1;
-    }
-    const int q0 = a.cu_new[lo], q1 = a.cu_new[lo + 1];
-    if (t < q0 || t >= q1 || q1 > a.T) return;      // behind the last request: left as it was
-    const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
-    long long seq = a.seq_lens[lo];
-    if (seq < 0 || seq > cap) {
-        if (lane == 0) report_status(a.status, LLAMA_ERR_CAPACITY);
-        seq = seq < 0 ? 0 : cap;
-    }
-    const long long keys = min(seq, seq - (q1 - q0) + (t - q0) + 1);
-    const int g = h / (a.nh / a.nkv);
-    const T* qp = static_cast<const T*>(a.q) + item * HD + lane * E;
-    float q[E], o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) { q[e] = to_f32<T>(qp[e]) * a.scale; o[e] = 0.f; }
-    for (long long j = 0; j < keys; ++j) {
-        const int page = a.block_tables[static_cast<long long>(lo) * a.max_pages + (j >> a.page_shift)];
-        float s = 0.f, v[E];
-        if (page < 0 || page >= a.n_pages) {
-            if (lane == 0) report_status(a.status, LLAMA_ERR_INVALID_ARG);
-#pragma unroll
-            for (int e = 0; e < E; ++e) v[e] = 0.f;
-        } else {
-            const long long at = ((((static_cast<long long>(page) * a.nkv + g) << a.page_shift) +
-                                   (j & ((1 << a.page_shift) - 1))) * HD) + lane * E;
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                s = fmaf(q[e], to_f32<T>(static_cast<const T*>(a.k_pages)[at + e]), s);
-                v[e] = to_f32<T>(static_cast<const T*>(a.v_pages)[at + e]);
-            }
-            s = warp_sum(s);
-        }
-        const float mn = fmaxf(m, s);
-        const float c = expf(m - mn), p = expf(s - mn);
-        l = l * c + p;
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(p, v[e], o[e] * c);
-        m = mn;
-    }
-    T* op = static_cast<T*>(a.out) + item * HD + lane * E;
-#pragma unroll
-    for (int e = 0; e < E; ++e) op[e] = from_f32<T>(keys > 0 ? o[e] / l : 0.f);
+namespace {
+constexpr int kThreads = 128;
+constexpr int kRows = 16;
+constexpr int kStages = 3;
+constexpr int kMaxCtas = 512;
+// Units per CTA below which fewer CTAs run: a split costs a publish and a merge.
+constexpr int kMinUnits = 4;
+
+template <typename T> constexpr int kUnitKeys = sizeof(T) == 2 ? 64 : 32;
+
+// Workspace: counters, (m, l) and o of two partial tiles per CTA.
+constexpr size_t kOffMl = kMaxCtas * sizeof(int);
+constexpr size_t kOffO = kOffMl + 2ull * kMaxCtas * kRows * sizeof(float2);
+constexpr size_t ws_bytes(int hd) { return kOffO + 2ull * kMaxCtas * kRows * hd * sizeof(float); }
+
+// Byte offset of 16-byte chunk `c` of row `row` in a unit's K or V block:
+// chunks are permuted within a row so that 8 rows read at one chunk index
+// (ldmatrix, or the fp32 score loop's rows two apart) fall into different banks.
+template <int ROW_BYTES>
+__device__ __forceinline__ uint32_t unit_off(int row, int c) {
+    if constexpr (ROW_BYTES == 64) return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
+    else return row * ROW_BYTES + ((c ^ (row & 7)) << 4);
 }
 
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+    const int n = ok ? 16 : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
+__device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr));
+}
 template <typename T>
-static int attn_hd(const PagedAttnArgs& a, cudaStream_t st) {
-    const long long blocks = (static_cast<long long>(a.T) * a.nh + 3) / 4;
-    const dim3 grid(static_cast<unsigned>(blocks));
-    if (a.hd == 32) paged_attn_kernel<T, 32><<<grid, 128, 0, st>>>(a);
-    else if (a.hd == 64) paged_attn_kernel<T, 64><<<grid, 128, 0, st>>>(a);
-    else paged_attn_kernel<T, 128><<<grid, 128, 0, st>>>(a);
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (std::is_same<T, bf16>::value)
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                     : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                     : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A value whose exponent bits are all ones: infinity or NaN.
+template <typename T> __device__ __forceinline__ bool not_finite16(uint32_t h) {
+    constexpr uint32_t e = std::is_same<T, bf16>::value ? 0x7f80u : 0x7c00u;
+    return (h & e) == e;
+}
+}  // namespace
+
+template <typename T, int HD>
+__global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a, TileShape shape) {
+    constexpr bool H16 = sizeof(T) == 2;
+    constexpr int KU = kUnitKeys<T>;
+    constexpr int ROW = HD * static_cast<int>(sizeof(T));
+    constexpr int BLK = KU * ROW;                 // K or V of a unit
+    constexpr int CPR = ROW / 16;                 // 16-byte chunks per row
+    constexpr int RPP = kThreads / CPR;           // rows one pass of the CTA copies
+    constexpr int NPG = KU / 16;                  // most pages of a unit
+    extern __shared__ __align__(128) uint8_t smem[];
+    // ring | scratch (16-bit: o of 4 warps x 4 rows; fp32: q, scores) | work list
+    constexpr int SCR = H16 ? 4 * 4 * HD * 4 : kRows * HD * 4 + kRows * KU * 4;
+    uint8_t* scr = smem + kStages * 2 * BLK;
+    long long* cum = reinterpret_cast<long long*>(scr + SCR);
+    WorkReq* req = reinterpret_cast<WorkReq*>(cum + a.B + 1);
+    __shared__ long long s_scan[kThreads / 32];
+    __shared__ float s_m[4][kRows], s_l[4][kRows], s_corr[kRows];
+    __shared__ int s_bad, s_last;
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
+    build_work<kThreads>(a.cu_new, a.seq_lens, a.B, a.T, cap, a.nkv, shape, req, cum, s_scan, a.status);
+    const long long W = cum[a.B];
+    const long long want = (W + kMinUnits - 1) / kMinUnits;
+    const int P = static_cast<int>(want < gridDim.x ? want : gridDim.x), c = blockIdx.x;
+    if (c >= P) return;
+    const long long u0 = run_start(c, W, P), u1 = run_start(c + 1, W, P);
+    const int len = static_cast<int>(u1 - u0);
+    const int rep = a.nh / a.nkv, lrep = 4 - shape.lr;      // 16 rows = 2^lr tokens * rep heads
+    const int R = 1 << shape.lr;
+
+    int* counters = static_cast<int*>(a.workspace);
+    float2* part_ml = reinterpret_cast<float2*>(static_cast<uint8_t*>(a.workspace) + kOffMl);
+    float* part_o = reinterpret_cast<float*>(static_cast<uint8_t*>(a.workspace) + kOffO);
+    const T* kp = static_cast<const T*>(a.k_pages);
+    const T* vp = static_cast<const T*>(a.v_pages);
+
+    // ---- copies: the cursor of the next unit to issue, and that unit's pages
+    WorkCur ic = work_at(shape, req, cum, a.B, a.nkv, u0);
+    int pg[NPG];
+    auto load_pages = [&]() {
+#pragma unroll
+        for (int i = 0; i < NPG; ++i) {
+            const long long key = static_cast<long long>(ic.j) * KU + i * 16;
+            const long long at = key >> a.page_shift;
+            pg[i] = ic.b < a.B && at < a.max_pages ? __ldg(a.block_tables + static_cast<long long>(ic.b) * a.max_pages + at) : -1;
+        }
+    };
+    auto issue = [&](int i) {                     // the i-th unit of the run
+        const WorkReq r = req[ic.b];
+        const int tok_end = min((ic.tile + 1) << shape.lr, r.n);
+        const long long kend = min(static_cast<long long>(r.seq), static_cast<long long>(r.seq) - r.n + tok_end);
+        const uint32_t base = smem_u32(smem + (i % kStages) * 2 * BLK);
+        const int ch = tid % CPR, r0 = tid / CPR;
+#pragma unroll
+        for (int p = 0; p < KU / RPP; ++p) {
+            const int row = p * RPP + r0;
+            const long long key = static_cast<long long>(ic.j) * KU + row;
+            int page = pg[0];
+#pragma unroll
+            for (int x = 1; x < NPG; ++x) page = (row >> 4) == x ? pg[x] : page;
+            const bool inside = page >= 0 && page < a.n_pages;
+            const bool ok = key < kend && inside;
+            if (key < kend && !inside && ch == 0) report_status(a.status, LLAMA_ERR_INVALID_ARG);
+            const long long off = ok ? (((static_cast<long long>(page) * a.nkv + ic.g) << a.page_shift) +
+                                        (key & ((1LL << a.page_shift) - 1))) * HD + ch * (16 / static_cast<int>(sizeof(T)))
+                                     : 0;
+            const uint32_t dst = base + unit_off<ROW>(row, ch);
+            cp16(dst, kp + off, ok);
+            cp16(dst + BLK, vp + off, ok);
+        }
+        if (++ic.j >= ic.nu) next_tile(shape, req, a.B, a.nkv, ic);
+    };
+    load_pages();
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < len) { issue(i); load_pages(); }
+        cp_commit();
+    }
+
+    // ---- the tile at hand
+    WorkCur cc = work_at(shape, req, cum, a.B, a.nkv, u0);
+    WorkReq rq = {0, 0, 0};
+    int t0 = 0, lim0 = 0, kend = 0;               // first token, keys its first and last row see
+    const float sl2 = a.scale * 1.4426950408889634f;
+    // keys that row r of the tile sees (<= 0: none); rows behind the request's last token see none
+    auto limit = [&](int r) {
+        const int t = t0 + (r >> lrep);
+        return t < rq.n ? min(rq.seq, rq.seq - rq.n + t + 1) : 0;
+    };
+    // 16-bit: lane (g = lane / 4, tq = lane % 4) holds rows g and g + 8
+    const int g8 = lane >> 2, tq = lane & 3;
+    uint32_t qa[H16 ? HD / 16 : 1][4];
+    float m2[2], l2[2], oacc[H16 ? HD / 8 : 1][4];
+    int lim2[2];
+    // fp32: q in shared memory; this warp's rows 4 warp .. +3 for the softmax,
+    // this thread's outputs: rows fr .. fr + FR - 1, columns fc .. fc + 3
+    constexpr int CG = HD / 4, RG = kThreads / CG, FR = kRows / RG;
+    const int fc = (tid % CG) * 4, fr = (tid / CG) * FR;
+    float mf[4], lf[4], of[H16 ? 1 : FR][4];
+    float* s_q = reinterpret_cast<float*>(scr);
+    float* s_p = s_q + kRows * HD;
+    auto start_tile = [&]() {
+        rq = req[cc.b];
+        t0 = cc.tile << shape.lr;
+        lim0 = limit(0);
+        kend = min(rq.seq, rq.seq - rq.n + min(t0 + R, rq.n));
+        if (tid == 0) s_bad = 0;
+        const T* qb = static_cast<const T*>(a.q);
+        auto qrow = [&](int r) {
+            return qb + (static_cast<long long>(rq.q0 + t0 + (r >> lrep)) * a.nh + cc.g * rep + (r & (rep - 1))) * HD;
+        };
+        if constexpr (H16) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int r = g8 + 8 * x;
+                const bool in = t0 + (r >> lrep) < rq.n;
+                const T* p = in ? qrow(r) : qb;
+#pragma unroll
+                for (int ks = 0; ks < HD / 16; ++ks) {
+                    qa[ks][x] = in ? *reinterpret_cast<const uint32_t*>(p + 16 * ks + 2 * tq) : 0u;
+                    qa[ks][2 + x] = in ? *reinterpret_cast<const uint32_t*>(p + 16 * ks + 2 * tq + 8) : 0u;
+                }
+                m2[x] = -INFINITY;
+                l2[x] = 0.f;
+                lim2[x] = limit(r);
+            }
+#pragma unroll
+            for (int nd = 0; nd < HD / 8; ++nd)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) oacc[nd][e] = 0.f;
+        } else {
+            for (int i = tid; i < kRows * (HD / 4); i += kThreads) {
+                const int r = i / (HD / 4), ch = i % (HD / 4);
+                float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (t0 + (r >> lrep) < rq.n) v = *reinterpret_cast<const float4*>(qrow(r) + ch * 4);
+                *reinterpret_cast<float4*>(s_q + r * HD + ((ch ^ ((r >> 1) & 7)) << 2)) = v;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) { mf[i] = -INFINITY; lf[i] = 0.f; }
+#pragma unroll
+            for (int i = 0; i < FR; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) of[i][e] = 0.f;
+        }
+    };
+    start_tile();
+    int seg_j0 = cc.j;                            // first unit of this CTA's part of the tile
+
+    for (int i = 0; i < len; ++i) {
+        cp_wait<kStages - 2>();
+        __syncthreads();                          // unit i landed; everyone is past unit i - 1
+        if (i + kStages - 1 < len) { issue(i + kStages - 1); load_pages(); }
+        cp_commit();
+        uint8_t* sK = smem + (i % kStages) * 2 * BLK;
+        uint8_t* sV = sK + BLK;
+        const int key0 = cc.j * KU;
+        const bool masked = key0 + KU > lim0;     // some row does not see some key
+        if (H16 && masked && kend > lim0) {
+            // A key that some rows see and others do not: a weight of 0 times
+            // an infinity or NaN of its V would reach the rows that do not see
+            // it.  Such values become 0 here and are added at the tile's end.
+            const int from = max(0, lim0 - key0);
+            for (int x = from * CPR + tid; x < KU * CPR; x += kThreads) {
+                uint32_t* p = reinterpret_cast<uint32_t*>(sV + x * 16);
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t v = p[w];
+                    const bool lo = not_finite16<T>(v & 0xffffu), hi = not_finite16<T>(v >> 16);
+                    if (lo || hi) {
+                        p[w] = v & ((lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u));
+                        s_bad = 1;
+                    }
+                }
+            }
+            __syncthreads();
+        }
+        if constexpr (H16) {
+            const uint32_t kb = smem_u32(sK), vb = smem_u32(sV);
+            const int mi = lane >> 3, rr = lane & 7;
+            float sc[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+            for (int ks = 0; ks < HD / 16; ++ks) {
+                uint32_t b[4];                    // keys 0-7: dims 0-7, 8-15; keys 8-15: dims 0-7, 8-15
+                ldsm4(kb + unit_off<ROW>(16 * warp + ((mi >> 1) << 3) + rr, 2 * ks + (mi & 1)), b);
+                mma16<T>(sc[0], qa[ks], b[0], b[1]);
+                mma16<T>(sc[1], qa[ks], b[2], b[3]);
+            }
+            uint32_t pa[4];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {         // rows g8 and g8 + 8
+                float s[4] = {sc[0][2 * x] * sl2, sc[0][2 * x + 1] * sl2, sc[1][2 * x] * sl2, sc[1][2 * x + 1] * sl2};
+                if (masked) {
+                    const int k0 = key0 + 16 * warp + 2 * tq;
+                    if (k0 >= lim2[x]) s[0] = -INFINITY;
+                    if (k0 + 1 >= lim2[x]) s[1] = -INFINITY;
+                    if (k0 + 8 >= lim2[x]) s[2] = -INFINITY;
+                    if (k0 + 9 >= lim2[x]) s[3] = -INFINITY;
+                }
+                float mx = fmaxf(fmaxf(s[0], s[1]), fmaxf(s[2], s[3]));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float mn = fmaxf(m2[x], mx);
+                const float ms = mn == -INFINITY ? 0.f : mn;     // no key so far: every weight is 0
+                const float corr = ex2(m2[x] - ms);
+                float p[4], rs = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) { p[e] = ex2(s[e] - ms); rs += p[e]; }
+                l2[x] = l2[x] * corr + rs;        // this lane's keys; summed over the quad at the end
+                m2[x] = mn;
+                pa[x] = pack2<T>(p[0], p[1]);
+                pa[2 + x] = pack2<T>(p[2], p[3]);
+#pragma unroll
+                for (int nd = 0; nd < HD / 8; ++nd) { oacc[nd][2 * x] *= corr; oacc[nd][2 * x + 1] *= corr; }
+            }
+#pragma unroll
+            for (int np = 0; np < HD / 16; ++np) {
+                uint32_t b[4];                    // dims 16 np ..: keys 0-7, 8-15; dims + 8: keys 0-7, 8-15
+                ldsm4_t(vb + unit_off<ROW>(16 * warp + ((mi & 1) << 3) + rr, 2 * np + (mi >> 1)), b);
+                mma16<T>(oacc[2 * np], pa, b[0], b[1]);
+                mma16<T>(oacc[2 * np + 1], pa, b[2], b[3]);
+            }
+        } else {
+            // scores: rows 2 (tid % 8) + {0, 1}, keys 2 (tid / 8) + {0, 1}
+            const int sr = (tid & 7) * 2, sk = (tid >> 3) * 2;
+            float s[2][2] = {{0.f, 0.f}, {0.f, 0.f}};
+#pragma unroll 4
+            for (int ch = 0; ch < HD / 4; ++ch) {
+                float4 q4[2], k4[2];
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    q4[x] = *reinterpret_cast<const float4*>(s_q + (sr + x) * HD + ((ch ^ ((sr >> 1) & 7)) << 2));
+                    k4[x] = *reinterpret_cast<const float4*>(sK + unit_off<ROW>(sk + x, ch));
+                }
+#pragma unroll
+                for (int x = 0; x < 2; ++x)
+#pragma unroll
+                    for (int y = 0; y < 2; ++y)
+                        s[x][y] = fmaf(q4[x].x, k4[y].x, fmaf(q4[x].y, k4[y].y, fmaf(q4[x].z, k4[y].z, fmaf(q4[x].w, k4[y].w, s[x][y]))));
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                *reinterpret_cast<float2*>(s_p + (sr + x) * KU + sk) = make_float2(s[x][0] * sl2, s[x][1] * sl2);
+            __syncthreads();
+            // softmax: rows 4 warp .. + 3, lane = key
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int r = 4 * warp + x;
+                const float v = key0 + lane < limit(r) ? s_p[r * KU + lane] : -INFINITY;
+                const float mn = fmaxf(mf[x], warp_max(v));
+                const float ms = mn == -INFINITY ? 0.f : mn;
+                const float p = ex2(v - ms), corr = ex2(mf[x] - ms);
+                lf[x] = lf[x] * corr + warp_sum(p);
+                mf[x] = mn;
+                s_p[r * KU + lane] = p;
+                if (lane == 0) s_corr[r] = corr;
+            }
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < FR; ++x) {
+                const float cr = s_corr[fr + x];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) of[x][e] *= cr;
+            }
+            int lims[FR];
+#pragma unroll
+            for (int x = 0; x < FR; ++x) lims[x] = limit(fr + x) - key0;
+#pragma unroll 4
+            for (int k = 0; k < KU; ++k) {
+                const float4 v = *reinterpret_cast<const float4*>(sV + unit_off<ROW>(k, fc >> 2));
+#pragma unroll
+                for (int x = 0; x < FR; ++x) {
+                    if (masked && k >= lims[x]) continue;        // not 0 times whatever the slot holds
+                    const float p = s_p[(fr + x) * KU + k];
+                    of[x][0] = fmaf(p, v.x, of[x][0]);
+                    of[x][1] = fmaf(p, v.y, of[x][1]);
+                    of[x][2] = fmaf(p, v.z, of[x][2]);
+                    of[x][3] = fmaf(p, v.w, of[x][3]);
+                }
+            }
+        }
+        if (cc.j + 1 < cc.nu && i + 1 < len) { ++cc.j; continue; }
+
+        // ---- end of the tile, or of this CTA's part of it
+        const bool whole = seg_j0 == 0 && cc.j + 1 == cc.nu;
+        const long long tile_u0 = u0 + i - cc.j;                 // the tile's first unit in the list
+        const int cf = whole ? c : run_of(tile_u0, W, P), cl = whole ? c : run_of(tile_u0 + cc.nu - 1, W, P);
+        const int slot = 2 * c + (c == cf ? 1 : 0);
+        const int rows = min(kRows, (rq.n - t0) << lrep);
+        auto out_at = [&](int r) {
+            return static_cast<T*>(a.out) +
+                   (static_cast<long long>(rq.q0 + t0 + (r >> lrep)) * a.nh + cc.g * rep + (r & (rep - 1))) * HD;
+        };
+        if constexpr (H16) {
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                l2[x] += __shfl_xor_sync(0xffffffffu, l2[x], 1);
+                l2[x] += __shfl_xor_sync(0xffffffffu, l2[x], 2);
+                if (tq == 0) { s_m[warp][g8 + 8 * x] = m2[x]; s_l[warp][g8 + 8 * x] = l2[x]; }
+            }
+            float* s_o = reinterpret_cast<float*>(scr);          // [4 warps][4 rows][HD]
+            for (int r0 = 0; r0 < rows; r0 += 4) {
+                __syncthreads();
+                if ((g8 >> 2) == ((r0 >> 2) & 1)) {
+                    const int x = r0 >> 3;                       // rows g8 or g8 + 8
+                    float* d = s_o + (warp * 4 + (g8 & 3)) * HD + 2 * tq;
+#pragma unroll
+                    for (int nd = 0; nd < HD / 8; ++nd)
+                        *reinterpret_cast<float2*>(d + 8 * nd) =
+                            x ? make_float2(oacc[nd][2], oacc[nd][3]) : make_float2(oacc[nd][0], oacc[nd][1]);
+                }
+                __syncthreads();
+                for (int idx = tid; idx < 4 * HD; idx += kThreads) {
+                    const int r = r0 + idx / HD, d = idx % HD;
+                    if (r >= rows) break;
+                    float M = -INFINITY, L = 0.f, acc = 0.f;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w][r]);
+                    const float Ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const float f = ex2(s_m[w][r] - Ms);
+                        L += s_l[w][r] * f;
+                        acc += s_o[(w * 4 + (r & 3)) * HD + d] * f;
+                    }
+                    const int lim = limit(r);
+                    if (s_bad) {                                 // infinities and NaN taken out of V above
+                        for (int k = max(lim0, seg_j0 * KU); k < min(lim, (cc.j + 1) * KU); ++k) {
+                            const int page = a.block_tables[static_cast<long long>(cc.b) * a.max_pages + (k >> a.page_shift)];
+                            if (k < 0 || page < 0 || page >= a.n_pages) continue;
+                            const float v = to_f32<T>(vp[(((static_cast<long long>(page) * a.nkv + cc.g) << a.page_shift) +
+                                                          (k & ((1 << a.page_shift) - 1))) * HD + d]);
+                            if (!(fabsf(v) < INFINITY)) acc += v;
+                        }
+                    }
+                    if (whole) {
+                        out_at(r)[d] = from_f32<T>(lim > 0 ? acc / L : 0.f);
+                    } else {
+                        part_o[(static_cast<long long>(slot) * kRows + r) * HD + d] = acc;
+                        if (d == 0) part_ml[slot * kRows + r] = make_float2(M, L);
+                    }
+                }
+            }
+        } else {
+            if (lane == 0) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x) { s_m[0][4 * warp + x] = mf[x]; s_l[0][4 * warp + x] = lf[x]; }
+            }
+            __syncthreads();
+#pragma unroll
+            for (int x = 0; x < FR; ++x) {
+                const int r = fr + x;
+                if (r >= rows) break;
+                if (whole) {
+                    const float inv = s_l[0][r];
+                    const bool some = limit(r) > 0;
+                    *reinterpret_cast<float4*>(out_at(r) + fc) =
+                        some ? make_float4(of[x][0] / inv, of[x][1] / inv, of[x][2] / inv, of[x][3] / inv)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
+                } else {
+                    *reinterpret_cast<float4*>(part_o + (static_cast<long long>(slot) * kRows + r) * HD + fc) =
+                        make_float4(of[x][0], of[x][1], of[x][2], of[x][3]);
+                    if (fc == 0) part_ml[slot * kRows + r] = make_float2(s_m[0][r], s_l[0][r]);
+                }
+            }
+        }
+        if (!whole) {
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const int seen = atomicAdd(counters + cf, 1);
+                s_last = seen == cl - cf;
+                if (s_last) counters[cf] = 0;
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                // contributor x in slot 2 x, the first one in slot 2 cf + 1
+                for (int idx = tid; idx < rows * (HD / 4); idx += kThreads) {
+                    const int r = idx / (HD / 4), d = (idx % (HD / 4)) * 4;
+                    float M = -INFINITY, L = 0.f;
+                    for (int x = cf; x <= cl; ++x) M = fmaxf(M, __ldcg(&part_ml[(2 * x + (x == cf)) * kRows + r].x));
+                    const float Ms = M == -INFINITY ? 0.f : M;
+                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                    for (int x = cf; x <= cl; ++x) {
+                        const long long s = static_cast<long long>(2 * x + (x == cf)) * kRows + r;
+                        const float2 ml = __ldcg(part_ml + s);
+                        const float4 v = __ldcg(reinterpret_cast<const float4*>(part_o + s * HD + d));
+                        const float f = ex2(ml.x - Ms);
+                        L += ml.y * f;
+                        o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+                    }
+                    const bool some = limit(r) > 0;
+                    T* dst = out_at(r) + d;
+                    const float4 y = some ? make_float4(o.x / L, o.y / L, o.z / L, o.w / L) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    if constexpr (H16) {
+                        uint2 w;
+                        w.x = pack2<T>(y.x, y.y);
+                        w.y = pack2<T>(y.z, y.w);
+                        *reinterpret_cast<uint2*>(dst) = w;
+                    } else {
+                        *reinterpret_cast<float4*>(dst) = y;
+                    }
+                }
+            }
+        }
+        if (i + 1 < len) {
+            __syncthreads();                      // s_m, s_l, s_q and the flags are reused
+            if (cc.j + 1 < cc.nu) ++cc.j; else next_tile(shape, req, a.B, a.nkv, cc);
+            start_tile();
+            seg_j0 = cc.j;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+template <typename T, int HD>
+static int attn_go(const PagedAttnArgs& a, cudaStream_t st) {
+    constexpr int KU = kUnitKeys<T>;
+    constexpr int ring = kStages * 2 * KU * HD * static_cast<int>(sizeof(T));
+    constexpr int scr = sizeof(T) == 2 ? 4 * 4 * HD * 4 : kRows * HD * 4 + kRows * KU * 4;
+    // the work list's room, in three sizes so that the occupancy is asked once for each
+    const int bucket = a.B <= 64 ? 0 : a.B <= 256 ? 1 : 2;
+    const int room = bucket == 0 ? 64 : bucket == 1 ? 256 : kPagedMaxRequests;
+    const int smem = ring + scr + (room + 1) * 8 + room * static_cast<int>(sizeof(WorkReq));
+    auto kern = paged_attn_kernel<T, HD>;
+    static int sms = 0, resident[3] = {0, 0, 0};
+    if (resident[bucket] == 0) {
+        int dev = 0, n = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem);
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged_attn_kernel)");
+        resident[bucket] = n < 1 ? 1 : n;
+    }
+    const int rep = a.nh / a.nkv;
+    TileShape shape;
+    shape.lr = rep == 1 ? 4 : rep == 2 ? 3 : rep == 4 ? 2 : 1;
+    shape.lk = KU == 64 ? 6 : 5;
+    // one resident wave, and no more CTAs than the step can have units
+    const long long cap = ((static_cast<long long>(a.max_pages) << a.page_shift) + KU - 1) / KU;
+    long long grid = static_cast<long long>(sms) * resident[bucket];
+    if (grid > kMaxCtas) grid = kMaxCtas;
+    const long long most = (static_cast<long long>(a.T) * a.nkv * cap + kMinUnits - 1) / kMinUnits;
+    if (grid > most) grid = most;
+    kern<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a, shape);
     LLB_CHECK_LAUNCH("paged_attn_kernel");
     return LLAMA_OK;
 }
 
-size_t paged_attention_ws(int, int, int, int, int) { return 256; }
+template <typename T>
+static int attn_hd(const PagedAttnArgs& a, cudaStream_t st) {
+    if (a.hd == 32) return attn_go<T, 32>(a, st);
+    if (a.hd == 64) return attn_go<T, 64>(a, st);
+    return attn_go<T, 128>(a, st);
+}
+
+size_t paged_attention_ws(int, int, int hd, int, int) { return (ws_bytes(hd) + 255) & ~size_t(255); }
 
 int launch_paged_attention(const PagedAttnArgs& a, int dtype, cudaStream_t st) {
     if (dtype == LLAMA_BF16) return attn_hd<bf16>(a, st);

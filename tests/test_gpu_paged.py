@@ -397,14 +397,17 @@ def test_attention_bad_tables_and_offsets(llb, dtype, hd, max_new):
     check(tables, [0, 2, 4, 6], [50, -4, 70], llb.LLAMA_ERR_CAPACITY, [0, 2])
     got = check(tables, [0, 2, 4, 900], seqs, llb.LLAMA_ERR_INVALID_ARG, [0, 1])
     assert (got[4:] == 7.0).all()
-    got = check(tables, [0, 2, 1, 6], [50, 60, 70], llb.LLAMA_ERR_INVALID_ARG, [0])
+    # request 1 ends before it starts and is skipped; request 2 starts inside request 0, whose row 1 both then hold
+    got = check(tables, [0, 2, 1, 6], [50, 60, 70], llb.LLAMA_ERR_INVALID_ARG, [])
+    want, tol = R.attention(q[:2], *dense[0], 2, seqs[0], hd ** -0.5)
+    assert ((got[0] - want[0]).abs() <= tol[0]).all()
 
 
 def test_attention_on_two_streams_and_in_graphs(llb):
     """Two captured calls with a workspace each, replayed at once on two streams beside eager calls."""
     g = torch.Generator().manual_seed(6)
     dt, page, nkv, nh, hd = torch.bfloat16, 16, 2, 16, 128
-    jobs = []
+    jobs, kept = [], []
     for new, seqs in (([1] * 20, [700 + 13 * i for i in range(20)]), ([300, 1], [900, 1200])):
         pools, tables, dense = paged_cache(seqs, page, nkv, hd, dt, g)
         q = torch.randn(sum(new), nh, hd, generator=g).to(dt)
@@ -420,6 +423,7 @@ def test_attention_on_two_streams_and_in_graphs(llb):
         with torch.cuda.graph(graph, stream=stream):
             llb.paged_attention(*a, out, max_new=max(new), workspace=ws)
         jobs.append((a, out, want, stream, graph, max(new)))
+        kept.append(ws)                               # a graph's workspace lives as long as the graph
     for _ in range(20):
         for a, out, want, stream, graph, mx in jobs:
             with torch.cuda.stream(stream):
