@@ -34,6 +34,7 @@ int cache_args(int T, int nh, int nkv, int hd, int dtype, int n_pages, int page_
     if (hd != 32 && hd != 64 && hd != 128) { set_error("head_dim %d unsupported (32, 64, 128)", hd); return LLAMA_ERR_INVALID_ARG; }
     if (nh > 1024) return bad("n_heads must be at most 1024");
     if (n_pages <= 0) return bad("n_pages must be positive");
+    if (static_cast<long long>(n_pages) * nkv > 0x7fffffffLL) return bad("n_pages * n_kv_heads must be below 2^31");
     *shift = page_shift_of(page_size);
     if (*shift < 0) { set_error("page_size %d must be 16, 32, 64, 128 or 256", page_size); return LLAMA_ERR_INVALID_ARG; }
     return LLAMA_OK;

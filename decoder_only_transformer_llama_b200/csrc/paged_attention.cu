@@ -555,9 +555,24 @@ static int attn_hd(const PagedAttnArgs& a, cudaStream_t st) {
     return attn_go<T, 128>(a, st);
 }
 
-size_t paged_attention_ws(int, int, int hd, int, int) { return (ws_bytes(hd) + 255) & ~size_t(255); }
+// Chunks take the tile kernel when a request's rows per KV head fill more than
+// two 16-row tiles (16-bit caches, head_dim 64 or 128).
+static bool tile_shape(int nh, int nkv, int hd, int dtype, int max_new) {
+    return dtype != LLAMA_F32 && hd != 32 && static_cast<long long>(max_new) * (nh / nkv) > 2 * kRows;
+}
+
+size_t paged_attention_ws(int nh, int nkv, int hd, int dtype, int max_new) {
+    size_t n = ws_bytes(hd);
+    if (tile_shape(nh, nkv, hd, dtype, max_new)) {
+        const size_t t = paged_attention_tile_ws(hd);
+        n = t > n ? t : n;
+    }
+    return (n + 255) & ~size_t(255);
+}
 
 int launch_paged_attention(const PagedAttnArgs& a, int dtype, cudaStream_t st) {
+    // the tile kernel scales after its row maximum, which needs a positive factor
+    if (tile_shape(a.nh, a.nkv, a.hd, dtype, a.max_new) && a.scale > 0.f) return launch_paged_attention_tile(a, dtype, st);
     if (dtype == LLAMA_BF16) return attn_hd<bf16>(a, st);
     if (dtype == LLAMA_F16) return attn_hd<f16>(a, st);
     return attn_hd<float>(a, st);
