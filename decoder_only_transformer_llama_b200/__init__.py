@@ -600,32 +600,55 @@ def op_linear(A, W, out, stream=None, workspace=None):
 
 
 # ---------------------------------------------------------------- a serving step over a paged KV cache
+# A step's calls are a few microseconds of device time each, so their checks
+# are kept to a handful of attribute reads per tensor.
 
-def _arg(t, dtype: str, shape, name: str, device):
-    """A contiguous tensor of torch dtype `dtype` and shape `shape` on `device` (None in `shape`: any size)."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if str(t.dtype) != "torch." + dtype:
-        raise ValueError(f"{name} must be {dtype}, not {t.dtype}")
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+_torch_module = None
 
 
-def _home(t, name: str):
-    """The device of a call's first tensor, which must be the current CUDA device (the stream's)."""
-    import torch
+def _torch():
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
+
+
+def _on(stream, torch, dev: int) -> int:
+    """The stream's handle; None: the device's current stream."""
+    if stream is not None:
+        return stream.cuda_stream
+    try:
+        return torch._C._cuda_getCurrentRawStream(dev)     # what torch.cuda.current_stream() wraps, 40 times as fast
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
+
+
+def _home(t, name: str, torch) -> int:
+    """Device index of a call's first tensor, which must be the current CUDA device (the stream's)."""
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.device
+    return t.get_device()
 
 
-def _status_arg(status, device):
-    if status is not None:
-        _arg(status, "int32", (1,), "status", device)
+def _arg(t, dtype, shape, name: str, dev: int):
+    """Checks a contiguous tensor of torch dtype `dtype` and shape `shape` on device `dev`; returns its address."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, not "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", strided"))
+    return t.data_ptr()
+
+
+def _table(t, rows: int, name: str, torch, dev: int):
+    """Checks an int32 [rows, any] table; returns its address and width."""
+    width = t.shape[1] if t.dim() == 2 else -1
+    return _arg(t, torch.int32, (rows, width), name, dev), width
+
+
+def _status_arg(status, torch, dev: int):
+    return None if status is None else _arg(status, torch.int32, (1,), "status", dev)
 
 
 def paged_plan(ctx_lens, new_lens, block_tables, free_pages, free_count, page_size: int, seq_lens, cu_new, slots,
@@ -636,50 +659,54 @@ def paged_plan(ctx_lens, new_lens, block_tables, free_pages, free_count, page_si
     free_pages [n_pages] and free_count [1] (the stack of free pages),
     cu_new [B+1], positions [T], free_left [1]; int64 slots [T].  seq_lens may
     be ctx_lens and free_left may be free_count: the step then updates them."""
-    dev = _home(ctx_lens, "ctx_lens")
-    B, T = ctx_lens.numel(), slots.numel()
-    _arg(ctx_lens, "int32", (B,), "ctx_lens", dev)
-    _arg(new_lens, "int32", (B,), "new_lens", dev)
-    _arg(block_tables, "int32", (B, None), "block_tables", dev)
-    _arg(free_pages, "int32", (None,), "free_pages", dev)
-    _arg(free_count, "int32", (1,), "free_count", dev)
-    _arg(seq_lens, "int32", (B,), "seq_lens", dev)
-    _arg(cu_new, "int32", (B + 1,), "cu_new", dev)
-    _arg(slots, "int64", (T,), "slots", dev)
-    _arg(positions, "int32", (T,), "positions", dev)
-    _arg(free_left, "int32", (1,), "free_left", dev)
-    _status_arg(status, dev)
-    _check(_lib.llama_paged_plan(ctx_lens.data_ptr(), new_lens.data_ptr(), B, page_size, block_tables.data_ptr(),
-                                 block_tables.shape[1], free_pages.data_ptr(), free_pages.numel(),
-                                 free_count.data_ptr(), T, seq_lens.data_ptr(), cu_new.data_ptr(), slots.data_ptr(),
-                                 positions.data_ptr(), free_left.data_ptr(), _ptr(status), _stream(stream)))
+    torch = _torch()
+    dev = _home(ctx_lens, "ctx_lens", torch)
+    i32 = torch.int32
+    B, T, n = ctx_lens.numel(), slots.numel(), free_pages.numel()
+    tables, width = _table(block_tables, B, "block_tables", torch, dev)
+    _check(_lib.llama_paged_plan(
+        _arg(ctx_lens, i32, (B,), "ctx_lens", dev), _arg(new_lens, i32, (B,), "new_lens", dev), B, page_size, tables,
+        width, _arg(free_pages, i32, (n,), "free_pages", dev), n, _arg(free_count, i32, (1,), "free_count", dev), T,
+        _arg(seq_lens, i32, (B,), "seq_lens", dev), _arg(cu_new, i32, (B + 1,), "cu_new", dev),
+        _arg(slots, torch.int64, (T,), "slots", dev), _arg(positions, i32, (T,), "positions", dev),
+        _arg(free_left, i32, (1,), "free_left", dev), _status_arg(status, torch, dev), _on(stream, torch, dev)))
 
 
 def rope_table(out, theta: float = 10000.0, stream=None):
     """Fills out, fp32 [len, head_dim/2, 2], with the rotation table that paged_append reads."""
-    dev = _home(out, "out")
-    _arg(out, "float32", (None, None, 2), "out", dev)
-    _check(_lib.llama_rope_table(out.data_ptr(), out.shape[0], 2 * out.shape[1], float(theta), _stream(stream)))
+    torch = _torch()
+    dev = _home(out, "out", torch)
+    _need(out.dim() == 3 and out.shape[2] == 2, "out must be [len, head_dim/2, 2]")
+    _check(_lib.llama_rope_table(_arg(out, torch.float32, out.shape, "out", dev), out.shape[0], 2 * out.shape[1],
+                                 float(theta), _on(stream, torch, dev)))
     return out
 
 
-def _rows(t, name: str, T: int, hd: int, device):
-    """A [T, heads, head_dim] view whose heads are contiguous; returns its row stride in elements."""
-    if t.device != device:
-        raise ValueError(f"{name} is on {t.device}, expected {device}")
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != hd:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({T}, heads, {hd})")
-    row = t.shape[1] * hd
-    if t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != hd):
-        raise ValueError(f"{name} must have contiguous heads")
-    return t.stride(0) if T > 1 else row
+def _rows(t, dtype, shape, name: str, dev: int):
+    """Checks a [T, heads, head_dim] view whose heads are contiguous; returns its address and row stride."""
+    T, heads, hd = shape
+    st = t.stride()
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or st[2] != 1 or (heads > 1 and st[1] != hd):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {tuple(shape)} with contiguous heads on cuda:{dev}, "
+                         f"not {t.dtype} {tuple(t.shape)} of strides {st} on {t.device}")
+    return t.data_ptr(), st[0] if T > 1 else heads * hd
 
 
-def _pools(k_pages, v_pages, dtype: str, device):
-    """(n_pages, n_kv_heads, page_size, head_dim) of a K and a V pool."""
-    _arg(k_pages, dtype, (None,) * 4, "k_pages", device)
-    _arg(v_pages, dtype, tuple(k_pages.shape), "v_pages", device)
-    return k_pages.shape
+def _pools(k_pages, v_pages, dtype, dev: int):
+    """Checks a K and a V pool [n_pages, n_kv_heads, page_size, head_dim]; returns their addresses and shape."""
+    shape = k_pages.shape
+    _need(len(shape) == 4, "k_pages must be [n_pages, n_kv_heads, page_size, head_dim]")
+    return _arg(k_pages, dtype, shape, "k_pages", dev), _arg(v_pages, dtype, shape, "v_pages", dev), shape
+
+
+def _code(dtype, torch, name: str) -> int:
+    if dtype is torch.bfloat16:
+        return LLAMA_BF16
+    if dtype is torch.float16:
+        return LLAMA_F16
+    if dtype is not torch.float32:
+        raise ValueError(f"{name} must be float32, bfloat16 or float16, not {dtype}")
+    return LLAMA_F32
 
 
 def paged_append(q, k, v, positions, slots, rope, q_out, k_pages, v_pages, q_norm=None, k_norm=None,
@@ -689,38 +716,36 @@ def paged_append(q, k, v, positions, slots, rope, q_out, k_pages, v_pages, q_nor
     [T, n_heads, head_dim], K and V to their `slots` of k_pages / v_pages
     [n_pages, n_kv_heads, page_size, head_dim] (llama_paged_append).  q, k, v
     are [T, heads, head_dim] views with any row stride, float32 or of the
-    cache's dtype."""
-    dev = _home(q, "q")
-    code = _dtype_code(q_out, "q_out")
-    dt = str(q_out.dtype)[6:]
-    n_pages, nkv, page, hd = _pools(k_pages, v_pages, dt, dev)
+    cache's dtype; positions int32 and slots int64 hold at least T entries."""
+    torch = _torch()
+    dev = _home(q, "q", torch)
+    dt, src, f32 = q_out.dtype, q.dtype, torch.float32
+    kp, vp, (n_pages, nkv, page, hd) = _pools(k_pages, v_pages, dt, dev)
+    _need(q.dim() == 3, "q must be [T, n_heads, head_dim]")
     T, nh = q.shape[0], q.shape[1]
-    sq, sk, sv = _rows(q, "q", T, hd, dev), _rows(k, "k", T, hd, dev), _rows(v, "v", T, hd, dev)
-    _need(k.shape[1] == nkv and v.shape[1] == nkv, "k and v must have the pool's heads")
-    _need(k.dtype == q.dtype and v.dtype == q.dtype, "q, k and v must have one dtype")
-    in_code = _dtype_code(q, "q")
-    _arg(q_out, dt, (T, nh, hd), "q_out", dev)
-    _arg(rope, "float32", (None, hd // 2, 2), "rope", dev)
-    _arg(positions, "int32", (None,), "positions", dev)
-    _arg(slots, "int64", (None,), "slots", dev)
-    _need(positions.numel() >= T and slots.numel() >= T, "positions and slots need an entry per row")
-    for w, name in ((q_norm, "q_norm"), (k_norm, "k_norm")):
-        if w is not None:
-            _arg(w, "float32", (hd,), name, dev)
-    _status_arg(status, dev)
-    _check(_lib.llama_paged_append(q.data_ptr(), sq, k.data_ptr(), sk, v.data_ptr(), sv, in_code, T, nh, nkv, hd,
-                                   _ptr(q_norm), _ptr(k_norm), float(eps), rope.data_ptr(), rope.shape[0],
-                                   positions.data_ptr(), slots.data_ptr(), q_out.data_ptr(), k_pages.data_ptr(),
-                                   v_pages.data_ptr(), n_pages, page, code, _ptr(status), _stream(stream)))
+    n = positions.numel()
+    _need(n >= T and slots.numel() >= T, "positions and slots need an entry per row")
+    _need(rope.dim() == 3, "rope must be [len, head_dim/2, 2]")
+    (qp, qs), (kq, ks), (vq, vs) = (_rows(q, src, (T, nh, hd), "q", dev), _rows(k, src, (T, nkv, hd), "k", dev),
+                                    _rows(v, src, (T, nkv, hd), "v", dev))
+    _check(_lib.llama_paged_append(
+        qp, qs, kq, ks, vq, vs, _code(src, torch, "q"), T, nh, nkv, hd,
+        None if q_norm is None else _arg(q_norm, f32, (hd,), "q_norm", dev),
+        None if k_norm is None else _arg(k_norm, f32, (hd,), "k_norm", dev), eps,
+        _arg(rope, f32, (rope.shape[0], hd // 2, 2), "rope", dev), rope.shape[0],
+        _arg(positions, torch.int32, (n,), "positions", dev),
+        _arg(slots, torch.int64, (slots.numel(),), "slots", dev), _arg(q_out, dt, (T, nh, hd), "q_out", dev), kp, vp,
+        n_pages, page, _code(dt, torch, "q_out"), _status_arg(status, torch, dev), _on(stream, torch, dev)))
     return q_out
 
 
 def paged_attention_workspace(q, n_kv_heads: int, max_new: int):
     """A zero-filled workspace for paged_attention calls on queries like q
     ([T, n_heads, head_dim]) with at most max_new new tokens per request.
-    Calls that share one must not overlap on the device."""
-    import torch
-    n = int(_lib.llama_paged_attention_workspace_bytes(q.shape[1], n_kv_heads, q.shape[2], _dtype_code(q, "q"),
+    Calls that share one must not overlap on the device, and it has to outlive
+    the graphs that captured it."""
+    torch = _torch()
+    n = int(_lib.llama_paged_attention_workspace_bytes(q.shape[1], n_kv_heads, q.shape[2], _code(q.dtype, torch, "q"),
                                                        max_new))
     if n == 0:
         raise LlamaError(LLAMA_ERR_INVALID_ARG, last_error())
@@ -734,31 +759,26 @@ def paged_attention(q, k_pages, v_pages, block_tables, cu_new, seq_lens, out, ma
     max_new: most new tokens of one request (None: T); scale: 1/sqrt(head_dim)
     if None.  workspace: paged_attention_workspace(), kept by the caller; None
     makes a new one for this call."""
-    dev = _home(q, "q")
-    code = _dtype_code(q, "q")
-    dt = str(q.dtype)[6:]
-    n_pages, nkv, page, hd = _pools(k_pages, v_pages, dt, dev)
+    torch = _torch()
+    dev = _home(q, "q", torch)
+    dt, i32 = q.dtype, torch.int32
+    kp, vp, (n_pages, nkv, page, hd) = _pools(k_pages, v_pages, dt, dev)
+    _need(q.dim() == 3 and q.shape[2] == hd, "q must be [T, n_heads, head_dim] of the pages' head_dim")
     T, nh = q.shape[0], q.shape[1]
-    _arg(q, dt, (T, nh, hd), "q", dev)
-    _arg(out, dt, (T, nh, hd), "out", dev)
     B = seq_lens.numel()
-    _arg(seq_lens, "int32", (B,), "seq_lens", dev)
-    _arg(cu_new, "int32", (B + 1,), "cu_new", dev)
-    _arg(block_tables, "int32", (B, None), "block_tables", dev)
-    _status_arg(status, dev)
+    tables, width = _table(block_tables, B, "block_tables", torch, dev)
     if max_new is None:
         max_new = max(T, 1)
     if workspace is None:
-        import torch
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             workspace = paged_attention_workspace(q, nkv, max_new)
-    else:
-        _arg(workspace, "uint8", (None,), "workspace", dev)
-    _check(_lib.llama_paged_attention(q.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), code, T, nh, nkv, hd, B,
-                                      cu_new.data_ptr(), seq_lens.data_ptr(), block_tables.data_ptr(),
-                                      block_tables.shape[1], n_pages, page, int(max_new),
-                                      float(scale) if scale is not None else hd ** -0.5, out.data_ptr(),
-                                      workspace.data_ptr(), workspace.numel(), _ptr(status), _stream(stream)))
+    ws_bytes = workspace.numel()
+    _check(_lib.llama_paged_attention(
+        _arg(q, dt, (T, nh, hd), "q", dev), kp, vp, _code(dt, torch, "q"), T, nh, nkv, hd, B,
+        _arg(cu_new, i32, (B + 1,), "cu_new", dev), _arg(seq_lens, i32, (B,), "seq_lens", dev), tables, width, n_pages,
+        page, max_new, hd ** -0.5 if scale is None else scale, _arg(out, dt, (T, nh, hd), "out", dev),
+        _arg(workspace, torch.uint8, (ws_bytes,), "workspace", dev), ws_bytes, _status_arg(status, torch, dev),
+        _on(stream, torch, dev)))
     return out
 
 
@@ -766,15 +786,15 @@ def sample_rows(logits, temperature, uniforms, out, top_k=None, top_p=None, min_
     """Next tokens with each row's own parameters (llama_sample_rows): fp32
     logits [B, V]; temperature, uniforms, top_p, min_p fp32 [B], top_k int32
     [B] (None: that filter is off); out int32 [B]."""
-    dev = _home(logits, "logits")
-    _arg(logits, "float32", (None, None), "logits", dev)
+    torch = _torch()
+    dev = _home(logits, "logits", torch)
+    f32, i32 = torch.float32, torch.int32
+    _need(logits.dim() == 2, "logits must be [B, V]")
     B, V = logits.shape
-    _arg(temperature, "float32", (B,), "temperature", dev)
-    _arg(uniforms, "float32", (B,), "uniforms", dev)
-    _arg(out, "int32", (B,), "out", dev)
-    for t, dt, name in ((top_k, "int32", "top_k"), (top_p, "float32", "top_p"), (min_p, "float32", "min_p")):
-        if t is not None:
-            _arg(t, dt, (B,), name, dev)
-    _check(_lib.llama_sample_rows(logits.data_ptr(), B, V, temperature.data_ptr(), _ptr(top_k), _ptr(top_p),
-                                  _ptr(min_p), uniforms.data_ptr(), out.data_ptr(), _stream(stream)))
+    _check(_lib.llama_sample_rows(
+        _arg(logits, f32, (B, V), "logits", dev), B, V, _arg(temperature, f32, (B,), "temperature", dev),
+        None if top_k is None else _arg(top_k, i32, (B,), "top_k", dev),
+        None if top_p is None else _arg(top_p, f32, (B,), "top_p", dev),
+        None if min_p is None else _arg(min_p, f32, (B,), "min_p", dev),
+        _arg(uniforms, f32, (B,), "uniforms", dev), _arg(out, i32, (B,), "out", dev), _on(stream, torch, dev)))
     return out
