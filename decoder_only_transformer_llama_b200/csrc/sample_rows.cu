@@ -12,21 +12,51 @@
 // exceeds u * Z: it lies in the kept prefix by itself, and no filter needs
 // the identity of its last token.  Masses are fp64 exponentials held as
 // 64-bit fixed point (2^-46 resolution): every prefix sum is an exact integer
-// in any order.
+// in any order, and tokens below 2^-47 of the maximum weigh nothing.
 //
-// One CTA per row; the prefix masses and the draw are found by a
-// most-significant-digit radix select over the 64-bit (logit, id) key, with
-// histograms of mass and count.
+// A row is spread over a cluster of 8 CTAs.  One histogram of mass and count
+// over 1024 equal steps of l_max - l (bins are ordered like the tokens), summed
+// over the cluster through distributed shared memory, turns each of the three
+// searches (k-th token, nucleus edge, draw) into the choice of a bin; the
+// tokens up to that bin, or in it, are gathered into a list of at most 256,
+// which every CTA resolves alike.  A bin with more tokens than that (ties, flat
+// rows) is first cut by histograms over 1024 steps of the order key, 10 bits
+// of it at a time.
 #include "common.cuh"
 #include "paged.h"
 
 namespace llb {
 
 namespace {
-constexpr int kThreads = 1024;
-constexpr double kFix = 70368744177664.0;     // 2^46: V * 2^46 < 2^64 for V <= 262144
-
 typedef unsigned long long u64;
+
+constexpr int kRanks = 8;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kBins = 1024;
+constexpr int kCap = 256;                     // tokens one list holds
+constexpr int kRegs = 8;                      // logits a thread keeps in registers (V <= 32768)
+constexpr double kFix = 70368744177664.0;     // 2^46: V * 2^46 < 2^64 for V <= 262144
+constexpr float kReach = 32.625f;             // 47 ln 2 = 32.58: masses beyond round to 0
+
+struct Prefix {
+    u64 mass[kBins + 1];                      // before each bin
+    unsigned int cnt[kBins + 1];
+};
+struct RowShared {
+    unsigned int h[4][kBins];                 // this CTA's histogram: counts, mass bits 0-15, 16-31, 32-46
+    Prefix p0, p1;                            // cluster totals: of the whole row, of a bin being cut
+    u64 seg_key[2][kCap], seg_mass[2][kCap];  // tokens this CTA gathered, read by the cluster
+    u64 key[kCap], mass[kCap];                // the cluster's list, ordered by bin
+    u64 x_max, x_s, x_zm;                     // this CTA's maximum key, mass and min-p mass, read by the cluster
+    float x_min;
+    int seg_n[2];
+    u64 red_a[kWarps], red_b[kWarps];
+    float red_f[kWarps];
+    double table[64];                         // 2^(-j / 64)
+    u64 res_before, res_key, res_mass;
+    int bin;
+};
 
 // Order key: larger for a larger logit, among equal logits for the lower id.
 // NaN orders with -inf: it is never drawn.  -0 and 0 are one value.
@@ -37,156 +67,444 @@ __device__ __forceinline__ u64 row_key(float l, int id) {
     u = (u & 0x80000000u) ? ~u : (u | 0x80000000u);
     return (static_cast<u64>(u) << 32) | static_cast<uint32_t>(~static_cast<uint32_t>(id));
 }
+__device__ __forceinline__ int key_id(u64 k) { return static_cast<int>(~static_cast<uint32_t>(k & 0xffffffffu)); }
+__device__ __forceinline__ float key_logit(u64 k) {
+    const uint32_t u = static_cast<uint32_t>(k >> 32);
+    return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
+}
 
-struct RowShared {
-    u64 mass[256];
-    unsigned int cnt[256];
-    float red_f[32];
-    u64 red_u[32];
-    u64 prefix, before;
-    unsigned int before_cnt;
-};
+__device__ __forceinline__ u64 ld_peer64(const void* p, uint32_t rank) {
+    u64 v;
+    asm volatile("ld.shared::cluster.u64 %0, [%1];" : "=l"(v) : "r"(cluster_addr(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ unsigned int ld_peer32(const void* p, uint32_t rank) {
+    unsigned int v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(cluster_addr(p, rank)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_peer64(const void* p, uint32_t rank, u64 v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(cluster_addr(p, rank)), "l"(v) : "memory");
+}
+__device__ __forceinline__ void st_peer32(const void* p, uint32_t rank, unsigned int v) {
+    asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(cluster_addr(p, rank)), "r"(v) : "memory");
+}
 
-struct RowParams {
+// One row's scales.  e = 2^(-y / 64), y = (l_max - l) * c64 with c64 = 64 log2(e) / T.
+struct Scale {
     float lmax;
-    double inv_t;
+    double c64;
+    float cbin;        // bins per unit of l_max - l
 };
 
-// e_i as a double; an infinite maximum leaves only its equals.
-__device__ __forceinline__ double row_exp(const RowParams& p, float l) {
-    if (!(l == l) || l == -INFINITY) return 0.0;
-    if (l == p.lmax) return 1.0;
-    if (p.lmax == INFINITY) return 0.0;
-    return exp((static_cast<double>(l) - static_cast<double>(p.lmax)) * p.inv_t);
+// e * 2^46 for a finite distance below the maximum: y = n + r, |r| <= 1/2, is cut into
+// n = 64 q + j, and 2^(-y/64) = 2^-q * 2^(-j/64) * exp(-r ln2 / 64) with the
+// exponential's Taylor terms up to the fifth power (|r ln2 / 64| < 0.0055: the
+// rest is below 4e-17).  Table-driven exponentials after Tang (1989).
+__device__ __forceinline__ double scaled_exp(const RowShared& sh, double y) {
+    constexpr double kMagic = 6755399441055744.0;              // 1.5 * 2^52: adding it rounds to an integer
+    const double t = y + kMagic;
+    const int n = static_cast<int>(__double_as_longlong(t) & 0xffffffffLL);
+    const double z = (t - kMagic - y) * (0.69314718055994530942 / 64.0);
+    double p = fma(z, 1.0 / 120.0, 1.0 / 24.0);
+    p = fma(p, z, 1.0 / 6.0);
+    p = fma(p, z, 0.5);
+    p = fma(p, z, 1.0);
+    p = fma(p, z, 1.0);
+    const double s = __longlong_as_double(static_cast<long long>(1023 + 46 - (n >> 6)) << 52);
+    return sh.table[n & 63] * p * s;
 }
-__device__ __forceinline__ u64 row_mass(const RowParams& p, float l) {
-    return static_cast<u64>(row_exp(p, l) * kFix + 0.5);
+// The mass of a logit, and whether min-p keeps it (e >= mp).
+__device__ __forceinline__ u64 row_mass(const RowShared& sh, const Scale& s, float l, double mp46, bool* keep) {
+    *keep = false;
+    if (!(l == l) || l == -INFINITY) return 0;
+    double e;
+    if (l == s.lmax) {
+        e = kFix;
+    } else {
+        const double y = (static_cast<double>(s.lmax) - static_cast<double>(l)) * s.c64;
+        if (!(y < 48.0 * 64.0)) { *keep = mp46 <= 0.0; return 0; }     // an infinite maximum too
+        e = scaled_exp(sh, y);
+    }
+    *keep = e >= mp46;
+    return static_cast<u64>(__double_as_longlong(e + 4503599627370496.0) & 0xfffffffffffffLL);   // + 2^52: rounds
+}
+__device__ __forceinline__ int row_bin(const Scale& s, float l) {
+    const float d = s.lmax - l;
+    if (!(d > 0.f)) return 0;                  // the maximum itself (infinite ones too)
+    const float y = d * s.cbin;
+    return y < static_cast<float>(kBins - 1) ? static_cast<int>(y) : kBins - 1;
 }
 
-// In sampling order, the first key whose inclusive mass exceeds `target`
-// (by_count: whose inclusive count exceeds it), or the last key; *before =
-// the mass of the keys ahead of it.
-__device__ u64 row_select(RowShared& sh, const float* row, int V, const RowParams& p, bool by_count, u64 target,
-                          u64* before_out) {
-    u64 prefix = 0, mask = 0, before = 0;
-    u64 before_cnt = 0;
-    for (int shift = 56; shift >= 0; shift -= 8) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < 256; i += kThreads) { sh.mass[i] = 0; sh.cnt[i] = 0; }
-        __syncthreads();
-        for (int i = threadIdx.x; i < V; i += kThreads) {
-            const float l = row[i];
-            const u64 key = row_key(l, i);
-            if ((key & mask) != prefix) continue;
-            const int bin = static_cast<int>((key >> shift) & 255u);
-            atomicAdd(&sh.mass[bin], row_mass(p, l));
-            atomicAdd(&sh.cnt[bin], 1u);
+// Adds a token to this CTA's histogram.
+__device__ __forceinline__ void hist_add(RowShared& sh, int bin, u64 m) {
+    atomicAdd(&sh.h[0][bin], 1u);
+    atomicAdd(&sh.h[1][bin], static_cast<unsigned int>(m & 0xffffu));
+    atomicAdd(&sh.h[2][bin], static_cast<unsigned int>((m >> 16) & 0xffffu));
+    atomicAdd(&sh.h[3][bin], static_cast<unsigned int>(m >> 32));
+}
+__device__ __forceinline__ void hist_clear(RowShared& sh) {
+    for (int i = threadIdx.x; i < 4 * kBins; i += kThreads) sh.h[i / kBins][i % kBins] = 0u;
+}
+
+// The cluster's totals of the histograms, as sums before each bin, into `p` of every CTA.
+__device__ void hist_reduce(RowShared& sh, Prefix& p, uint32_t rank) {
+    cluster_sync();
+    {
+        // CTA r adds up bins [128 r, 128 r + 128): four threads a bin, two CTAs each
+        const int bin = static_cast<int>(rank) * (kBins / kRanks) + (threadIdx.x >> 2), q = threadIdx.x & 3;
+        u64 m = 0;
+        unsigned int c = 0;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            const uint32_t from = 2 * q + x;
+            c += ld_peer32(&sh.h[0][bin], from);
+            m += ld_peer32(&sh.h[1][bin], from) + (static_cast<u64>(ld_peer32(&sh.h[2][bin], from)) << 16) +
+                 (static_cast<u64>(ld_peer32(&sh.h[3][bin], from)) << 32);
         }
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            u64 cm = before, cc = before_cnt, bm = before, bc = before_cnt;
-            int chosen = -1;
-            for (int bin = 255; bin >= 0; --bin) {
-                if (!sh.cnt[bin]) continue;
-                chosen = bin;
-                bm = cm;
-                bc = cc;
-                cm += sh.mass[bin];
-                cc += sh.cnt[bin];
-                if ((by_count ? cc : cm) > target) break;
-            }
-            sh.prefix = prefix | (static_cast<u64>(chosen) << shift);
-            sh.before = bm;
-            sh.before_cnt = static_cast<unsigned int>(bc);
+#pragma unroll
+        for (int o = 1; o < 4; o <<= 1) {
+            m += __shfl_xor_sync(0xffffffffu, m, o);
+            c += __shfl_xor_sync(0xffffffffu, c, o);
         }
-        __syncthreads();
-        prefix = sh.prefix;
-        before = sh.before;
-        before_cnt = sh.before_cnt;
-        mask |= 255ull << shift;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+            st_peer64(&p.mass[bin + 1], 2 * q + x, m);
+            st_peer32(&p.cnt[bin + 1], 2 * q + x, c);
+        }
     }
-    *before_out = before;
-    return prefix;
+    cluster_sync();
+    // prefix sums: two bins a thread
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = 2 * threadIdx.x;
+    const u64 m0 = p.mass[b + 1], m1 = p.mass[b + 2];
+    const unsigned int c0 = p.cnt[b + 1], c1 = p.cnt[b + 2];
+    u64 m = m0 + m1;
+    unsigned int c = c0 + c1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const u64 ym = __shfl_up_sync(0xffffffffu, m, o);
+        const unsigned int yc = __shfl_up_sync(0xffffffffu, c, o);
+        if (lane >= o) { m += ym; c += yc; }
+    }
+    if (lane == 31) { sh.red_a[warp] = m; sh.red_b[warp] = c; }
+    __syncthreads();
+    u64 bm = m - m0 - m1;
+    unsigned int bc = c - c0 - c1;
+    for (int w = 0; w < warp; ++w) { bm += sh.red_a[w]; bc += static_cast<unsigned int>(sh.red_b[w]); }
+    p.mass[b + 1] = bm + m0;
+    p.cnt[b + 1] = bc + c0;
+    p.mass[b + 2] = bm + m0 + m1;
+    p.cnt[b + 2] = bc + c0 + c1;
+    if (threadIdx.x == 0) { p.mass[0] = 0; p.cnt[0] = 0; }
+    __syncthreads();
+}
+
+// The bin that holds the first token whose inclusive mass (by_count: count)
+// exceeds `target`, counted from `p`'s first bin; the caller knows there is one.
+__device__ __forceinline__ int choose_bin(RowShared& sh, const Prefix& p, bool by_count, u64 target) {
+    for (int b = threadIdx.x; b < kBins; b += kThreads) {
+        const u64 lo = by_count ? p.cnt[b] : p.mass[b], hi = by_count ? p.cnt[b + 1] : p.mass[b + 1];
+        if (lo <= target && target < hi) sh.bin = b;
+    }
+    __syncthreads();
+    const int bin = sh.bin;
+    __syncthreads();
+    return bin;
 }
 }  // namespace
 
-__global__ void __launch_bounds__(kThreads)
+// REG: a thread's logits of its CTA's slice stay in registers (V <= 32768);
+// otherwise each pass reads them again (from L2).
+template <bool REG>
+__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
 sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restrict__ temperature,
                    const int32_t* __restrict__ top_k, const float* __restrict__ top_p,
                    const float* __restrict__ min_p, const float* __restrict__ uniforms, int32_t* __restrict__ out) {
-    __shared__ RowShared sh;
-    const int b = blockIdx.x;
-    const float* row = logits + static_cast<long long>(b) * V;
+    extern __shared__ __align__(16) uint8_t smem[];
+    RowShared& sh = *reinterpret_cast<RowShared*>(smem);
+    const uint32_t rank = cluster_rank();
+    const int b = blockIdx.x / kRanks;
     const float T = temperature[b];
     const int k = top_k ? top_k[b] : 0;
     const float tp = top_p ? top_p[b] : 1.f;
     const float mp = min_p ? min_p[b] : 0.f;
     if (!(T >= 0.f) || T == INFINITY || !(tp >= 0.f) || !(mp >= 0.f) || mp > 1.f) {
-        if (threadIdx.x == 0) out[b] = -1;
-        return;
+        if (rank == 0 && threadIdx.x == 0) out[b] = -1;
+        return;                                // the whole cluster, before any exchange
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int S = (V + kRanks - 1) / kRanks, lo = static_cast<int>(rank) * S;
+    const int n = max(0, min(S, V - lo));
+    const float* row = logits + static_cast<long long>(b) * V + lo;
+    float reg[REG ? kRegs : 1];
+    if constexpr (REG) {
+#pragma unroll
+        for (int e = 0; e < kRegs; ++e) {
+            const int j = threadIdx.x + e * kThreads;
+            reg[e] = j < n ? row[j] : -INFINITY;
+        }
+    }
+    // f(logit, id) for every token of the slice
+    auto each = [&](auto f) {
+        if constexpr (REG) {
+#pragma unroll
+            for (int e = 0; e < kRegs; ++e) {
+                const int j = threadIdx.x + e * kThreads;
+                if (j < n) f(reg[e], lo + j);
+            }
+        } else {
+#pragma unroll 4
+            for (int j = threadIdx.x; j < n; j += kThreads) f(__ldg(row + j), lo + j);
+        }
+    };
+
+    // ---- the largest key of the row and its smallest finite logit
+    if (threadIdx.x < 64) sh.table[threadIdx.x] = exp2(-static_cast<double>(threadIdx.x) / 64.0);
+    hist_clear(sh);
     u64 best = 0;
-    for (int i = threadIdx.x; i < V; i += kThreads) {
-        const u64 key = row_key(row[i], i);
+    float least = INFINITY;
+    each([&](float l, int id) {
+        const u64 key = row_key(l, id);
         best = key > best ? key : best;
-    }
+        if (l > -INFINITY && l < least) least = l;
+    });
     best = warp_max_u64(best);
-    if (lane == 0) sh.red_u[warp] = best;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
+    if (lane == 0) { sh.red_a[warp] = best; sh.red_f[warp] = least; }
     __syncthreads();
-    for (int w = 0; w < kThreads / 32; ++w) best = sh.red_u[w] > best ? sh.red_u[w] : best;
-    const int first = static_cast<int>(~static_cast<uint32_t>(best & 0xffffffffu));
-    RowParams p;
-    p.lmax = row[first];
-    if (!(p.lmax == p.lmax)) p.lmax = -INFINITY;
-    if (T == 0.f || p.lmax == -INFINITY) {
-        if (threadIdx.x == 0) out[b] = first;
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kWarps; ++w) {
+            best = sh.red_a[w] > best ? sh.red_a[w] : best;
+            least = fminf(least, sh.red_f[w]);
+        }
+        sh.x_max = best;
+        sh.x_min = least;
+    }
+    cluster_sync();
+    {
+        u64 m = lane < kRanks ? ld_peer64(&sh.x_max, lane) : 0ull;
+        float f = lane < kRanks ? __uint_as_float(ld_peer32(&sh.x_min, lane)) : INFINITY;
+        best = warp_max_u64(m);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) f = fminf(f, __shfl_xor_sync(0xffffffffu, f, o));
+        least = f;
+    }
+    Scale sc;
+    sc.lmax = key_logit(best);
+    if (T == 0.f || sc.lmax == -INFINITY) {
+        if (rank == 0 && threadIdx.x == 0) out[b] = key_id(best);
+        cluster_sync();                        // no CTA leaves while its shared memory may be read
         return;
     }
-    p.inv_t = 1.0 / static_cast<double>(T);
-    __syncthreads();
-    // all tokens, and those of min-p
+    sc.c64 = 64.0 * 1.4426950408889634074 / static_cast<double>(T);
+    const float reach = fminf(kReach * T, sc.lmax - least);
+    sc.cbin = reach > 0.f ? static_cast<float>(kBins) / reach : 0.f;
+    if (!(sc.cbin < INFINITY)) sc.cbin = 3e38f;
+
+    // ---- histogram of the row; its mass and min-p's
+    const double mp46 = static_cast<double>(mp) * kFix;
     u64 s = 0, zm = 0;
-    for (int i = threadIdx.x; i < V; i += kThreads) {
-        const double e = row_exp(p, row[i]);
-        const u64 m = static_cast<u64>(e * kFix + 0.5);
+    each([&](float l, int) {
+        bool keep;
+        const u64 m = row_mass(sh, sc, l, mp46, &keep);
+        if (m == 0) return;
         s += m;
-        if (e >= static_cast<double>(mp)) zm += m;
-    }
+        if (keep) zm += m;
+        hist_add(sh, row_bin(sc, l), m);
+    });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) {
         s += __shfl_xor_sync(0xffffffffu, s, o);
         zm += __shfl_xor_sync(0xffffffffu, zm, o);
     }
-    __shared__ u64 s_m[32];
-    if (lane == 0) { sh.red_u[warp] = s; s_m[warp] = zm; }
+    if (lane == 0) { sh.red_a[warp] = s; sh.red_b[warp] = zm; }
     __syncthreads();
-    s = 0;
-    zm = 0;
-    for (int w = 0; w < kThreads / 32; ++w) { s += sh.red_u[w]; zm += s_m[w]; }
-    u64 z = s, before;
-    if (k > 0 && k < V) {
-        const u64 key = row_select(sh, row, V, p, true, static_cast<u64>(k - 1), &before);
-        z = before + row_mass(p, row[~static_cast<uint32_t>(key & 0xffffffffu)]);
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kWarps; ++w) zm += sh.red_b[w];
+        sh.x_zm = zm;
+    }
+    hist_reduce(sh, sh.p0, rank);
+    s = sh.p0.mass[kBins];
+    {
+        u64 m = lane < kRanks ? ld_peer64(&sh.x_zm, lane) : 0ull;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+        zm = __shfl_sync(0xffffffffu, m, 0);
+    }
+
+    // ---- searches
+    int turn = 0;                              // list buffer of the next gather
+    int have_lo = 1, have_hi = 0;              // bins of the row's histogram the list holds
+    u64 list_mass = 0;                         // mass before the list
+    unsigned int list_cnt = 0;
+    int list_n = 0;
+    // Gathers the tokens that `in` accepts (at most kCap over the cluster) into
+    // sh.key / sh.mass of every CTA.
+    auto gather = [&](auto in) {
+        if (threadIdx.x == 0) sh.seg_n[turn] = 0;
+        __syncthreads();
+        each([&](float l, int id) {
+            const u64 key = row_key(l, id);
+            if (!in(l, key)) return;
+            bool keep;
+            const u64 m = row_mass(sh, sc, l, 0.0, &keep);
+            if (m == 0) return;
+            const int at = atomicAdd(&sh.seg_n[turn], 1);
+            sh.seg_key[turn][at] = key;
+            sh.seg_mass[turn][at] = m;
+        });
+        cluster_sync();
+        const int mine = lane < kRanks ? static_cast<int>(ld_peer32(&sh.seg_n[turn], lane)) : 0;
+        int at = 0;
+        for (uint32_t r = 0; r < kRanks; ++r) {
+            const int c = __shfl_sync(0xffffffffu, mine, r);
+            for (int i = threadIdx.x; i < c; i += kThreads) {
+                sh.key[at + i] = ld_peer64(&sh.seg_key[turn][i], r);
+                sh.mass[at + i] = ld_peer64(&sh.seg_mass[turn][i], r);
+            }
+            at += c;
+        }
+        list_n = at;
+        turn ^= 1;
+        __syncthreads();
+    };
+    // The first token whose inclusive mass (by_count: count) exceeds `target`
+    // (there is one): its key, mass and the mass before it in sh.res_*.
+    auto find = [&](bool by_count, u64 target) {
+        const int bin = choose_bin(sh, sh.p0, by_count, target);
+        if (bin < have_lo || bin > have_hi) {
+            const unsigned int upto = sh.p0.cnt[bin + 1], within = upto - sh.p0.cnt[bin];
+            if (upto <= kCap) {
+                have_lo = 0;
+                have_hi = bin;
+                gather([&](float l, u64) { return row_bin(sc, l) <= bin; });
+            } else if (within <= kCap) {
+                have_lo = have_hi = bin;
+                gather([&](float l, u64) { return row_bin(sc, l) == bin; });
+            } else {
+                have_lo = 1;                   // a list of part of a bin serves no other search
+                have_hi = 0;
+            }
+            if (have_lo <= have_hi) {
+                list_mass = sh.p0.mass[have_lo];
+                list_cnt = sh.p0.cnt[have_lo];
+            } else {
+                // cut the bin by its order keys [k0, k1]
+                u64 k1 = 0, k0 = ~0ull;
+                each([&](float l, int id) {
+                    bool keep;
+                    if (row_bin(sc, l) != bin || row_mass(sh, sc, l, 0.0, &keep) == 0) return;
+                    const u64 key = row_key(l, id);
+                    k1 = key > k1 ? key : k1;
+                    k0 = key < k0 ? key : k0;
+                });
+                k1 = warp_max_u64(k1);
+                k0 = ~warp_max_u64(~k0);
+                if (lane == 0) { sh.red_a[warp] = k1; sh.red_b[warp] = k0; }
+                __syncthreads();
+                if (threadIdx.x == 0) {
+                    for (int w = 1; w < kWarps; ++w) {
+                        k1 = sh.red_a[w] > k1 ? sh.red_a[w] : k1;
+                        k0 = sh.red_b[w] < k0 ? sh.red_b[w] : k0;
+                    }
+                    sh.x_max = k1;
+                    sh.x_s = k0;
+                }
+                cluster_sync();
+                k1 = warp_max_u64(lane < kRanks ? ld_peer64(&sh.x_max, lane) : 0ull);
+                k0 = ~warp_max_u64(lane < kRanks ? ~ld_peer64(&sh.x_s, lane) : 0ull);
+                list_mass = sh.p0.mass[bin];
+                list_cnt = sh.p0.cnt[bin];
+                unsigned int inside = within;
+                while (inside > kCap) {
+                    const int bits = 64 - __clzll(static_cast<long long>(k1 - k0));
+                    const int shift = bits > 10 ? bits - 10 : 0;
+                    __syncthreads();
+                    hist_clear(sh);
+                    __syncthreads();
+                    each([&](float l, int id) {
+                        const u64 key = row_key(l, id);
+                        if (key < k0 || key > k1) return;
+                        bool keep;
+                        const u64 m = row_mass(sh, sc, l, 0.0, &keep);
+                        if (m) hist_add(sh, static_cast<int>((k1 - key) >> shift), m);
+                    });
+                    hist_reduce(sh, sh.p1, rank);
+                    const int cut = choose_bin(sh, sh.p1, by_count, target - (by_count ? list_cnt : list_mass));
+                    list_mass += sh.p1.mass[cut];
+                    list_cnt += sh.p1.cnt[cut];
+                    inside = sh.p1.cnt[cut + 1] - sh.p1.cnt[cut];
+                    const u64 top = k1 - (static_cast<u64>(cut) << shift);
+                    const u64 low = top - ((1ull << shift) - 1);
+                    k0 = low > k0 && low <= top ? low : k0;
+                    k1 = top;
+                }
+                gather([&](float, u64 key) { return key >= k0 && key <= k1; });
+            }
+        }
+        // place the token in the list: what lies before it in the list
+        for (int i = threadIdx.x; i < list_n; i += kThreads) {
+            const u64 key = sh.key[i], m = sh.mass[i];
+            u64 bm = list_mass;
+            unsigned int bc = list_cnt;
+            for (int j = 0; j < list_n; ++j) {
+                const bool ahead = sh.key[j] > key;
+                bm += ahead ? sh.mass[j] : 0ull;
+                bc += ahead;
+            }
+            if (by_count ? bc == target : bm <= target && target < bm + m) {
+                sh.res_before = bm;
+                sh.res_key = key;
+                sh.res_mass = m;
+            }
+        }
+        __syncthreads();
+    };
+    u64 z = s;
+    if (k > 0 && static_cast<unsigned int>(k) < sh.p0.cnt[kBins]) {
+        find(true, static_cast<u64>(k - 1));
+        z = sh.res_before + sh.res_mass;
+        __syncthreads();
     }
     if (tp < 1.f) {
         const u64 target = static_cast<u64>(static_cast<double>(tp) * static_cast<double>(z));
-        const u64 key = row_select(sh, row, V, p, false, target, &before);
-        const u64 zp = before + row_mass(p, row[~static_cast<uint32_t>(key & 0xffffffffu)]);
-        z = zp < z ? zp : z;
+        if (target < s) {                      // the edge; never short of the first token
+            find(false, target);
+            const u64 zp = sh.res_before + sh.res_mass;
+            z = zp < z ? zp : z;
+            __syncthreads();
+        }
     }
     z = zm < z ? zm : z;
     // u below 1, so the target stays below the kept mass
     const double u = fmin(fmax(static_cast<double>(uniforms[b]), 0.0), 1.0 - 1.0 / 16777216.0);
-    const u64 key = row_select(sh, row, V, p, false, static_cast<u64>(u * static_cast<double>(z)), &before);
-    if (threadIdx.x == 0) out[b] = static_cast<int32_t>(~static_cast<uint32_t>(key & 0xffffffffu));
+    find(false, static_cast<u64>(u * static_cast<double>(z)));
+    if (rank == 0 && threadIdx.x == 0) out[b] = key_id(sh.res_key);
+    cluster_sync();                            // no CTA leaves while its shared memory may be read
+}
+
+template <bool REG>
+static int rows_go(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
+                   const float* top_p, const float* min_p, const float* uniforms, int32_t* out, cudaStream_t st) {
+    static bool attr = false;
+    if (!attr) {
+        cudaError_t e = cudaFuncSetAttribute(sample_rows_kernel<REG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             static_cast<int>(sizeof(RowShared)));
+        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(sample_rows_kernel)");
+        attr = true;
+    }
+    sample_rows_kernel<REG><<<B * kRanks, kThreads, sizeof(RowShared), st>>>(logits, V, temperature, top_k, top_p, min_p,
+                                                                           uniforms, out);
+    LLB_CHECK_LAUNCH("sample_rows_kernel");
+    return LLAMA_OK;
 }
 
 int launch_sample_rows(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
                        const float* top_p, const float* min_p, const float* uniforms, int32_t* out, cudaStream_t st) {
-    sample_rows_kernel<<<B, kThreads, 0, st>>>(logits, V, temperature, top_k, top_p, min_p, uniforms, out);
-    LLB_CHECK_LAUNCH("sample_rows_kernel");
-    return LLAMA_OK;
+    if (V <= kRanks * kThreads * kRegs)
+        return rows_go<true>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
+    return rows_go<false>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
 }
 
 }  // namespace llb
