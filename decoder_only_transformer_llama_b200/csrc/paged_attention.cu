@@ -55,7 +55,11 @@ __device__ __forceinline__ uint32_t unit_off(int row, int c) {
     else return row * ROW_BYTES + ((c ^ (row & 7)) << 4);
 }
 
-__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+// With zeros in place of the source's bytes unless `ok`.
+__device__ __forceinline__ void cp16_if(uint32_t dst, const void* src, bool ok) {
     const int n = ok ? 16 : 0;
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" :: "r"(dst), "l"(src), "r"(n) : "memory");
 }
@@ -110,16 +114,17 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
     uint8_t* scr = smem + kStages * 2 * BLK;
     long long* cum = reinterpret_cast<long long*>(scr + SCR);
     WorkReq* req = reinterpret_cast<WorkReq*>(cum + a.B + 1);
-    __shared__ long long s_scan[kThreads / 32];
+    __shared__ long long s_scan[2 * kThreads / 32], s_tiles;
     __shared__ float s_m[4][kRows], s_l[4][kRows], s_corr[kRows];
     __shared__ int s_bad, s_last;
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
-    build_work<kThreads>(a.cu_new, a.seq_lens, a.B, a.T, cap, a.nkv, shape, req, cum, s_scan, a.status);
+    build_work<kThreads>(a.cu_new, a.seq_lens, a.B, a.T, cap, a.nkv, shape, req, cum, s_scan, &s_tiles, a.status);
     const long long W = cum[a.B];
-    const long long want = (W + kMinUnits - 1) / kMinUnits;
-    const int P = static_cast<int>(want < gridDim.x ? want : gridDim.x), c = blockIdx.x;
+    // a CTA for every kMinUnits units or every tile, whichever is more
+    const long long parts = max((W + kMinUnits - 1) / kMinUnits, min(s_tiles, W));
+    const int P = static_cast<int>(parts < gridDim.x ? parts : gridDim.x), c = blockIdx.x;
     if (c >= P) return;
     const long long u0 = run_start(c, W, P), u1 = run_start(c + 1, W, P);
     const int len = static_cast<int>(u1 - u0);
@@ -132,41 +137,67 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
     const T* kp = static_cast<const T*>(a.k_pages);
     const T* vp = static_cast<const T*>(a.v_pages);
 
-    // ---- copies: the cursor of the next unit to issue, and that unit's pages
+    // ---- copies: the cursor of the next unit to issue, its tile's last key and its pages
     WorkCur ic = work_at(shape, req, cum, a.B, a.nkv, u0);
-    int pg[NPG];
+    int pg[NPG], ikend = 0;
+    const int32_t* itable = nullptr;
+    auto issue_tile = [&]() {
+        if (ic.b >= a.B) return;
+        const WorkReq r = req[ic.b];
+        ikend = min(r.seq, r.seq - r.n + min((ic.tile + 1) << shape.lr, r.n));
+        itable = a.block_tables + static_cast<long long>(ic.b) * a.max_pages;
+    };
+    issue_tile();
     auto load_pages = [&]() {
 #pragma unroll
         for (int i = 0; i < NPG; ++i) {
-            const long long key = static_cast<long long>(ic.j) * KU + i * 16;
-            const long long at = key >> a.page_shift;
-            pg[i] = ic.b < a.B && at < a.max_pages ? __ldg(a.block_tables + static_cast<long long>(ic.b) * a.max_pages + at) : -1;
+            const int at = (ic.j * KU + i * 16) >> a.page_shift;
+            pg[i] = ic.b < a.B && at < a.max_pages ? __ldg(itable + at) : -1;
         }
     };
+    const int ch = tid % CPR, r0 = tid / CPR;     // this thread's 16-byte chunk and first row
+    const long long page_elems = static_cast<long long>(HD) << a.page_shift;
     auto issue = [&](int i) {                     // the i-th unit of the run
-        const WorkReq r = req[ic.b];
-        const int tok_end = min((ic.tile + 1) << shape.lr, r.n);
-        const long long kend = min(static_cast<long long>(r.seq), static_cast<long long>(r.seq) - r.n + tok_end);
         const uint32_t base = smem_u32(smem + (i % kStages) * 2 * BLK);
-        const int ch = tid % CPR, r0 = tid / CPR;
+        const int left = ikend - ic.j * KU;       // keys of the unit that exist
+        bool inside = true;
+        long long off[NPG];                       // elements to this thread's chunk in each 16 rows
 #pragma unroll
-        for (int p = 0; p < KU / RPP; ++p) {
-            const int row = p * RPP + r0;
-            const long long key = static_cast<long long>(ic.j) * KU + row;
-            int page = pg[0];
-#pragma unroll
-            for (int x = 1; x < NPG; ++x) page = (row >> 4) == x ? pg[x] : page;
-            const bool inside = page >= 0 && page < a.n_pages;
-            const bool ok = key < kend && inside;
-            if (key < kend && !inside && ch == 0) report_status(a.status, LLAMA_ERR_INVALID_ARG);
-            const long long off = ok ? (((static_cast<long long>(page) * a.nkv + ic.g) << a.page_shift) +
-                                        (key & ((1LL << a.page_shift) - 1))) * HD + ch * (16 / static_cast<int>(sizeof(T)))
-                                     : 0;
-            const uint32_t dst = base + unit_off<ROW>(row, ch);
-            cp16(dst, kp + off, ok);
-            cp16(dst + BLK, vp + off, ok);
+        for (int x = 0; x < NPG; ++x) {
+            inside = inside && static_cast<unsigned>(pg[x]) < static_cast<unsigned>(a.n_pages);
+            off[x] = (static_cast<long long>(pg[x]) * a.nkv + ic.g) * page_elems +
+                     ((ic.j * KU + x * 16) & ((1 << a.page_shift) - 1)) * HD + ch * (16 / static_cast<int>(sizeof(T)));
         }
-        if (++ic.j >= ic.nu) next_tile(shape, req, a.B, a.nkv, ic);
+        auto group = [&](int p) {                 // offset of the 16 rows that pass p's row lies in
+            if constexpr (RPP <= 16) return off[p * RPP / 16];
+            else return (r0 & 16) ? off[2 * p + 1] : off[2 * p];
+        };
+        if (inside && left >= KU) {
+#pragma unroll
+            for (int p = 0; p < KU / RPP; ++p) {
+                const long long o = group(p) + ((p * RPP + r0) & 15) * HD;
+                const uint32_t dst = base + unit_off<ROW>(p * RPP + r0, ch);
+                cp16(dst, kp + o);
+                cp16(dst + BLK, vp + o);
+            }
+        } else {
+            // the request's last unit, or a page outside the pool: rows that do not exist read as zeros
+#pragma unroll
+            for (int p = 0; p < KU / RPP; ++p) {
+                const int row = p * RPP + r0;
+                int page = pg[0];
+#pragma unroll
+                for (int x = 1; x < NPG; ++x) page = (row >> 4) == x ? pg[x] : page;
+                const bool known = static_cast<unsigned>(page) < static_cast<unsigned>(a.n_pages);
+                const bool ok = row < left && known;
+                if (row < left && !known && ch == 0) report_status(a.status, LLAMA_ERR_INVALID_ARG);
+                const long long o = ok ? group(p) + (row & 15) * HD : 0;
+                const uint32_t dst = base + unit_off<ROW>(row, ch);
+                cp16_if(dst, kp + o, ok);
+                cp16_if(dst + BLK, vp + o, ok);
+            }
+        }
+        if (++ic.j >= ic.nu) { next_tile(shape, req, a.B, a.nkv, ic); issue_tile(); }
     };
     load_pages();
 #pragma unroll
@@ -178,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
     // ---- the tile at hand
     WorkCur cc = work_at(shape, req, cum, a.B, a.nkv, u0);
     WorkReq rq = {0, 0, 0};
-    int t0 = 0, lim0 = 0, kend = 0;               // first token, keys its first and last row see
+    int t0 = 0, lim0 = 0, kend = 0, rows = 0;     // first token, keys its first and last row see, rows in use
     const float sl2 = a.scale * 1.4426950408889634f;
     // keys that row r of the tile sees (<= 0: none); rows behind the request's last token see none
     auto limit = [&](int r) {
@@ -202,6 +233,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
         t0 = cc.tile << shape.lr;
         lim0 = limit(0);
         kend = min(rq.seq, rq.seq - rq.n + min(t0 + R, rq.n));
+        rows = min(kRows, (rq.n - t0) << lrep);
         if (tid == 0) s_bad = 0;
         const T* qb = static_cast<const T*>(a.q);
         auto qrow = [&](int r) {
@@ -283,9 +315,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
                 mma16<T>(sc[0], qa[ks], b[0], b[1]);
                 mma16<T>(sc[1], qa[ks], b[2], b[3]);
             }
-            uint32_t pa[4];
+            uint32_t pa[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
             for (int x = 0; x < 2; ++x) {         // rows g8 and g8 + 8
+                if (x == 1 && rows <= 8) break;
                 float s[4] = {sc[0][2 * x] * sl2, sc[0][2 * x + 1] * sl2, sc[1][2 * x] * sl2, sc[1][2 * x + 1] * sl2};
                 if (masked) {
                     const int k0 = key0 + 16 * warp + 2 * tq;
@@ -307,8 +340,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
                 m2[x] = mn;
                 pa[x] = pack2<T>(p[0], p[1]);
                 pa[2 + x] = pack2<T>(p[2], p[3]);
+                if (__any_sync(0xffffffffu, corr != 1.f)) {      // some row's maximum moved
 #pragma unroll
-                for (int nd = 0; nd < HD / 8; ++nd) { oacc[nd][2 * x] *= corr; oacc[nd][2 * x + 1] *= corr; }
+                    for (int nd = 0; nd < HD / 8; ++nd) { oacc[nd][2 * x] *= corr; oacc[nd][2 * x + 1] *= corr; }
+                }
             }
 #pragma unroll
             for (int np = 0; np < HD / 16; ++np) {
@@ -383,7 +418,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
         const long long tile_u0 = u0 + i - cc.j;                 // the tile's first unit in the list
         const int cf = whole ? c : run_of(tile_u0, W, P), cl = whole ? c : run_of(tile_u0 + cc.nu - 1, W, P);
         const int slot = 2 * c + (c == cf ? 1 : 0);
-        const int rows = min(kRows, (rq.n - t0) << lrep);
         auto out_at = [&](int r) {
             return static_cast<T*>(a.out) +
                    (static_cast<long long>(rq.q0 + t0 + (r >> lrep)) * a.nh + cc.g * rep + (r & (rep - 1))) * HD;
@@ -472,32 +506,66 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                // contributor x in slot 2 x, the first one in slot 2 cf + 1
-                for (int idx = tid; idx < rows * (HD / 4); idx += kThreads) {
-                    const int r = idx / (HD / 4), d = (idx % (HD / 4)) * 4;
+                // Contributor x published in slot 2 x, the first one in slot 2 cf + 1.
+                // Per row: the maximum and the weighted sum by a warp, lane = contributor;
+                // then the outputs, a thread holding four columns of kMine rows, with
+                // the weights of kMergeStep contributors at a time in shared memory.
+                auto slot_of = [&](int x) { return static_cast<long long>(2 * x + (x == cf ? 1 : 0)) * kRows; };
+                for (int r = warp; r < rows; r += kThreads / 32) {
                     float M = -INFINITY, L = 0.f;
-                    for (int x = cf; x <= cl; ++x) M = fmaxf(M, __ldcg(&part_ml[(2 * x + (x == cf)) * kRows + r].x));
+                    for (int x = cf + lane; x <= cl; x += 32) M = fmaxf(M, __ldcg(&part_ml[slot_of(x) + r].x));
+                    M = warp_max(M);
                     const float Ms = M == -INFINITY ? 0.f : M;
-                    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                    for (int x = cf; x <= cl; ++x) {
-                        const long long s = static_cast<long long>(2 * x + (x == cf)) * kRows + r;
-                        const float2 ml = __ldcg(part_ml + s);
-                        const float4 v = __ldcg(reinterpret_cast<const float4*>(part_o + s * HD + d));
-                        const float f = ex2(ml.x - Ms);
-                        L += ml.y * f;
-                        o.x += v.x * f; o.y += v.y * f; o.z += v.z * f; o.w += v.w * f;
+                    for (int x = cf + lane; x <= cl; x += 32) {
+                        const float2 ml = __ldcg(&part_ml[slot_of(x) + r]);
+                        L += ml.y * ex2(ml.x - Ms);
                     }
+                    L = warp_sum(L);
+                    if (lane == 0) { s_m[0][r] = Ms; s_l[0][r] = L; }
+                }
+                constexpr int kMergeStep = 64;
+                constexpr int kMine = kRows * (HD / 4) / kThreads;
+                float* s_f = reinterpret_cast<float*>(scr);      // [kMergeStep][kRows]
+                float4 o[kMine];
+#pragma unroll
+                for (int y = 0; y < kMine; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+                for (int x0 = cf; x0 <= cl; x0 += kMergeStep) {
+                    const int nx = min(kMergeStep, cl + 1 - x0);
+                    __syncthreads();
+                    for (int idx = tid; idx < nx * kRows; idx += kThreads) {
+                        const int r = idx % kRows;
+                        if (r < rows) s_f[idx] = ex2(__ldcg(&part_ml[slot_of(x0 + idx / kRows) + r].x) - s_m[0][r]);
+                    }
+                    __syncthreads();
+#pragma unroll
+                    for (int y = 0; y < kMine; ++y) {
+                        const int idx = tid + y * kThreads, r = idx / (HD / 4), d = (idx % (HD / 4)) * 4;
+                        if (r >= rows) break;
+#pragma unroll 8
+                        for (int x = 0; x < nx; ++x) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(part_o + (slot_of(x0 + x) + r) * HD + d));
+                            const float f = s_f[x * kRows + r];
+                            o[y].x = fmaf(v.x, f, o[y].x); o[y].y = fmaf(v.y, f, o[y].y);
+                            o[y].z = fmaf(v.z, f, o[y].z); o[y].w = fmaf(v.w, f, o[y].w);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int y = 0; y < kMine; ++y) {
+                    const int idx = tid + y * kThreads, r = idx / (HD / 4), d = (idx % (HD / 4)) * 4;
+                    if (r >= rows) break;
+                    const float L = s_l[0][r];
                     const bool some = limit(r) > 0;
                     T* dst = out_at(r) + d;
-                    const float4 y = some ? make_float4(o.x / L, o.y / L, o.z / L, o.w / L) : make_float4(0.f, 0.f, 0.f, 0.f);
+                    const float4 v = some ? make_float4(o[y].x / L, o[y].y / L, o[y].z / L, o[y].w / L)
+                                          : make_float4(0.f, 0.f, 0.f, 0.f);
                     if constexpr (H16) {
                         uint2 w;
-                        w.x = pack2<T>(y.x, y.y);
-                        w.y = pack2<T>(y.z, y.w);
+                        w.x = pack2<T>(v.x, v.y);
+                        w.y = pack2<T>(v.z, v.w);
                         *reinterpret_cast<uint2*>(dst) = w;
                     } else {
-                        *reinterpret_cast<float4*>(dst) = y;
+                        *reinterpret_cast<float4*>(dst) = v;
                     }
                 }
             }
@@ -541,7 +609,7 @@ static int attn_go(const PagedAttnArgs& a, cudaStream_t st) {
     const long long cap = ((static_cast<long long>(a.max_pages) << a.page_shift) + KU - 1) / KU;
     long long grid = static_cast<long long>(sms) * resident[bucket];
     if (grid > kMaxCtas) grid = kMaxCtas;
-    const long long most = (static_cast<long long>(a.T) * a.nkv * cap + kMinUnits - 1) / kMinUnits;
+    const long long most = static_cast<long long>(a.T) * a.nkv * cap;
     if (grid > most) grid = most;
     kern<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(a, shape);
     LLB_CHECK_LAUNCH("paged_attn_kernel");

@@ -94,16 +94,17 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
     WorkReq* req = reinterpret_cast<WorkReq*>(cum + a.B + 1);
     __shared__ uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots];
     __shared__ uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], mdone;
-    __shared__ long long s_scan[kThreads / 32];
+    __shared__ long long s_scan[2 * kThreads / 32], s_tiles;
     __shared__ uint32_t tmem_slot;
     __shared__ int s_fail, s_bad, s_last[2];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const long long cap = static_cast<long long>(a.max_pages) << a.page_shift;
-    build_work<kThreads>(a.cu_new, a.seq_lens, a.B, a.T, cap, a.nkv, shape, req, cum, s_scan, a.status);
+    build_work<kThreads>(a.cu_new, a.seq_lens, a.B, a.T, cap, a.nkv, shape, req, cum, s_scan, &s_tiles, a.status);
     const long long W = cum[a.B];
-    const long long want = (W + kMinUnits - 1) / kMinUnits;
-    const int P = static_cast<int>(want < gridDim.x ? want : gridDim.x), cta = blockIdx.x;
+    // a CTA for every kMinUnits units or every tile, whichever is more
+    const long long parts = max((W + kMinUnits - 1) / kMinUnits, min(s_tiles, W));
+    const int P = static_cast<int>(parts < gridDim.x ? parts : gridDim.x), cta = blockIdx.x;
     if (cta >= P) return;                          // the whole CTA, before any barrier or TMEM
     const long long u0 = run_start(cta, W, P), u1 = run_start(cta + 1, W, P);
     const int rep = a.nh / a.nkv, lrep = 8 - shape.lr;
@@ -577,7 +578,7 @@ static int tile_go(const PagedAttnArgs& a, int dtype, cudaStream_t st) {
     shape.lr = rep == 1 ? 8 : rep == 2 ? 7 : rep == 4 ? 6 : 5;
     shape.lk = 7;
     const long long cap = ((static_cast<long long>(a.max_pages) << a.page_shift) + kKeys - 1) / kKeys;
-    long long grid = (static_cast<long long>(a.T) * a.nkv * cap + kMinUnits - 1) / kMinUnits;
+    long long grid = static_cast<long long>(a.T) * a.nkv * cap;
     if (grid > sms) grid = sms;
     kern<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(mq, mk, mv, a, shape, nslots);
     LLB_CHECK_LAUNCH("paged_attn_tile_kernel");

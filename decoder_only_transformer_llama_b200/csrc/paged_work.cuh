@@ -55,10 +55,17 @@ __host__ __device__ __forceinline__ int tile_at(TileShape s, int ctx, int n, lon
     return lo;
 }
 
-__host__ __device__ __forceinline__ long long run_start(long long c, long long W, long long P) { return c * W / P; }
+// (32-bit divisions where the products fit: a 64-bit one takes about 100 instructions)
+__host__ __device__ __forceinline__ long long run_start(long long c, long long W, long long P) {
+    const long long x = c * W;
+    if (x <= 0xffffffffLL) return static_cast<uint32_t>(x) / static_cast<uint32_t>(P);
+    return x / P;
+}
 // The run that holds unit u.
 __host__ __device__ __forceinline__ int run_of(long long u, long long W, long long P) {
-    return static_cast<int>(((u + 1) * P - 1) / W);
+    const long long x = (u + 1) * P - 1;
+    if (x <= 0xffffffffLL && W <= 0xffffffffLL) return static_cast<int>(static_cast<uint32_t>(x) / static_cast<uint32_t>(W));
+    return static_cast<int>(x / W);
 }
 
 // One request as the kernels hold it in shared memory.
@@ -74,15 +81,16 @@ struct WorkCur {
 #ifdef __CUDACC__
 // Fills req[0 .. B) and cum[0 .. B] (units before each request) from the
 // call's offsets and lengths, with the checks of the entry point; CTA 0
-// reports.  All NT threads of the CTA; scratch: NT / 32 values.
+// reports.  All NT threads of the CTA; scratch: 2 NT / 32 values.  *tiles = the
+// tiles of all requests and heads.
 template <int NT>
 __device__ __forceinline__ void build_work(const int32_t* cu, const int32_t* seq_lens, int B, int T, long long cap,
                                            int nkv, TileShape shape, WorkReq* req, long long* cum, long long* scratch,
-                                           int* status) {
+                                           long long* tiles, int* status) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int per = (B + NT - 1) / NT;
     const int b0 = threadIdx.x * per;
-    long long mine = 0;
+    long long mine = 0, my_tiles = 0;
     for (int b = b0; b < b0 + per && b < B; ++b) {
         const int q0 = cu[b], q1 = cu[b + 1];
         int seq = seq_lens[b], n = q1 - q0;
@@ -96,6 +104,7 @@ __device__ __forceinline__ void build_work(const int32_t* cu, const int32_t* seq
         }
         req[b] = {q0, n, seq};
         mine += request_units(shape, seq > n ? seq - n : 0, n) * nkv;
+        my_tiles += static_cast<long long>(tiles_of(shape, n)) * nkv;
         cum[b + 1] = mine;
     }
     long long incl = mine;
@@ -104,12 +113,19 @@ __device__ __forceinline__ void build_work(const int32_t* cu, const int32_t* seq
         const long long y = __shfl_up_sync(0xffffffffu, incl, o);
         if (lane >= o) incl += y;
     }
-    if (lane == 31) scratch[warp] = incl;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) my_tiles += __shfl_xor_sync(0xffffffffu, my_tiles, o);
+    if (lane == 31) { scratch[warp] = incl; scratch[NT / 32 + warp] = my_tiles; }
     __syncthreads();
     long long before = incl - mine;
     for (int w = 0; w < warp; ++w) before += scratch[w];
     for (int b = b0; b < b0 + per && b < B; ++b) cum[b + 1] += before;
-    if (threadIdx.x == 0) cum[0] = 0;
+    if (threadIdx.x == 0) {
+        cum[0] = 0;
+        long long t = 0;
+        for (int w = 0; w < NT / 32; ++w) t += scratch[NT / 32 + w];
+        *tiles = t;
+    }
     __syncthreads();
 }
 
@@ -123,11 +139,12 @@ __device__ __forceinline__ WorkCur work_at(TileShape s, const WorkReq* req, cons
         if (cum[mid] <= u) lo = mid; else hi = mid - 1;
     }
     const WorkReq r = req[lo];
-    const long long per = (cum[lo + 1] - cum[lo]) / nkv;
+    const long long per = request_units(s, ctx_of(r), r.n);
     const long long rem = u - cum[lo];
     WorkCur c;
     c.b = lo;
-    c.g = static_cast<int>(rem / per);
+    c.g = rem <= 0xffffffffLL && per <= 0xffffffffLL ? static_cast<uint32_t>(rem) / static_cast<uint32_t>(per)
+                                                     : static_cast<int>(rem / per);
     const long long v = rem - c.g * per;
     c.tile = tile_at(s, ctx_of(r), r.n, v);
     c.j = static_cast<int>(v - tiles_units(s, ctx_of(r), c.tile));
