@@ -14,14 +14,16 @@
 // 64-bit fixed point (2^-46 resolution): every prefix sum is an exact integer
 // in any order, and tokens below 2^-47 of the maximum weigh nothing.
 //
-// A row is spread over a cluster of 8 CTAs.  One histogram of mass and count
-// over 1024 equal steps of l_max - l (bins are ordered like the tokens), summed
-// over the cluster through distributed shared memory, turns each of the three
-// searches (k-th token, nucleus edge, draw) into the choice of a bin; the
-// tokens up to that bin, or in it, are gathered into a list of at most 256,
-// which every CTA resolves alike.  A bin with more tokens than that (ties, flat
-// rows) is first cut by histograms over 1024 steps of the order key, 10 bits
-// of it at a time.
+// A row is spread over a cluster of 8 CTAs.  A histogram over 1024 equal steps
+// of l_max - l (bins are ordered like the tokens), summed over the cluster
+// through distributed shared memory, turns each of the three searches (k-th
+// token, nucleus edge, draw) into the choice of a bin; the tokens up to that
+// bin, or in it, are gathered into a list of at most 256, which every CTA sorts
+// and resolves alike.  A row with a small top_k needs counts only: its list
+// holds every token that may be drawn, and only their exponentials are taken.
+// Other rows add masses to the histogram.  A bin with more tokens than a list
+// holds (ties, flat rows) is cut by histograms over 1024 steps of the order key,
+// 10 bits of it at a time.
 #include "common.cuh"
 #include "paged.h"
 
@@ -35,8 +37,9 @@ constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kCap = 256;                     // tokens one list holds
-constexpr int kRegs = 8;                      // logits a thread keeps in registers (V <= 32768)
+constexpr int kKept = 4096;                   // logits of a slice that stay in shared memory (V <= 32768)
 constexpr double kFix = 70368744177664.0;     // 2^46: V * 2^46 < 2^64 for V <= 262144
+constexpr u64 kKeep = 1ull << 63;             // beside a mass: min-p keeps the token
 constexpr float kReach = 32.625f;             // 47 ln 2 = 32.58: masses beyond round to 0
 
 struct Prefix {
@@ -47,15 +50,17 @@ struct RowShared {
     unsigned int h[4][kBins];                 // this CTA's histogram: counts, mass bits 0-15, 16-31, 32-46
     Prefix p0, p1;                            // cluster totals: of the whole row, of a bin being cut
     u64 seg_key[2][kCap], seg_mass[2][kCap];  // tokens this CTA gathered, read by the cluster
-    u64 key[kCap], mass[kCap];                // the cluster's list, ordered by bin
-    u64 x_max, x_s, x_zm;                     // this CTA's maximum key, mass and min-p mass, read by the cluster
-    float x_min;
+    u64 key[kCap], mass[kCap];                // the cluster's list as gathered
+    u64 s_key[kCap], s_pre[kCap + 1];         // and in sampling order: keys, mass before each (and behind the last)
+    u64 x_zm, x_k0, x_k1;                     // this CTA's part of a maximum or sum, read by the cluster
+    float x_max, x_min;
+    int x_id;
+    bool s_keep[kCap];                        // min-p keeps it
     int seg_n[2];
     u64 red_a[kWarps], red_b[kWarps];
-    float red_f[kWarps];
+    float red_f[kWarps], red_g[kWarps];
     double table[64];                         // 2^(-j / 64)
-    u64 res_before, res_key, res_mass;
-    int bin;
+    int bin, hit;
 };
 
 // Order key: larger for a larger logit, among equal logits for the lower id.
@@ -68,10 +73,6 @@ __device__ __forceinline__ u64 row_key(float l, int id) {
     return (static_cast<u64>(u) << 32) | static_cast<uint32_t>(~static_cast<uint32_t>(id));
 }
 __device__ __forceinline__ int key_id(u64 k) { return static_cast<int>(~static_cast<uint32_t>(k & 0xffffffffu)); }
-__device__ __forceinline__ float key_logit(u64 k) {
-    const uint32_t u = static_cast<uint32_t>(k >> 32);
-    return __uint_as_float((u & 0x80000000u) ? (u & 0x7fffffffu) : ~u);
-}
 
 __device__ __forceinline__ u64 ld_peer64(const void* p, uint32_t rank) {
     u64 v;
@@ -148,6 +149,7 @@ __device__ __forceinline__ void hist_clear(RowShared& sh) {
 }
 
 // The cluster's totals of the histograms, as sums before each bin, into `p` of every CTA.
+template <bool MASS>
 __device__ void hist_reduce(RowShared& sh, Prefix& p, uint32_t rank) {
     cluster_sync();
     {
@@ -159,8 +161,9 @@ __device__ void hist_reduce(RowShared& sh, Prefix& p, uint32_t rank) {
         for (int x = 0; x < 2; ++x) {
             const uint32_t from = 2 * q + x;
             c += ld_peer32(&sh.h[0][bin], from);
-            m += ld_peer32(&sh.h[1][bin], from) + (static_cast<u64>(ld_peer32(&sh.h[2][bin], from)) << 16) +
-                 (static_cast<u64>(ld_peer32(&sh.h[3][bin], from)) << 32);
+            if (MASS)
+                m += ld_peer32(&sh.h[1][bin], from) + (static_cast<u64>(ld_peer32(&sh.h[2][bin], from)) << 16) +
+                     (static_cast<u64>(ld_peer32(&sh.h[3][bin], from)) << 32);
         }
 #pragma unroll
         for (int o = 1; o < 4; o <<= 1) {
@@ -169,14 +172,14 @@ __device__ void hist_reduce(RowShared& sh, Prefix& p, uint32_t rank) {
         }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-            st_peer64(&p.mass[bin + 1], 2 * q + x, m);
+            if (MASS) st_peer64(&p.mass[bin + 1], 2 * q + x, m);
             st_peer32(&p.cnt[bin + 1], 2 * q + x, c);
         }
     }
     cluster_sync();
     // prefix sums: two bins a thread
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, b = 2 * threadIdx.x;
-    const u64 m0 = p.mass[b + 1], m1 = p.mass[b + 2];
+    const u64 m0 = MASS ? p.mass[b + 1] : 0ull, m1 = MASS ? p.mass[b + 2] : 0ull;
     const unsigned int c0 = p.cnt[b + 1], c1 = p.cnt[b + 2];
     u64 m = m0 + m1;
     unsigned int c = c0 + c1;
@@ -213,9 +216,9 @@ __device__ __forceinline__ int choose_bin(RowShared& sh, const Prefix& p, bool b
 }
 }  // namespace
 
-// REG: a thread's logits of its CTA's slice stay in registers (V <= 32768);
-// otherwise each pass reads them again (from L2).
-template <bool REG>
+// KEPT: the CTA's slice of the row stays in shared memory (V <= 32768);
+// otherwise each pass reads it again (from L2).
+template <bool KEPT>
 __global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
 sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restrict__ temperature,
                    const int32_t* __restrict__ top_k, const float* __restrict__ top_p,
@@ -236,123 +239,87 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     const int S = (V + kRanks - 1) / kRanks, lo = static_cast<int>(rank) * S;
     const int n = max(0, min(S, V - lo));
     const float* row = logits + static_cast<long long>(b) * V + lo;
-    float reg[REG ? kRegs : 1];
-    if constexpr (REG) {
-#pragma unroll
-        for (int e = 0; e < kRegs; ++e) {
-            const int j = threadIdx.x + e * kThreads;
-            reg[e] = j < n ? row[j] : -INFINITY;
-        }
-    }
+    float* kept = reinterpret_cast<float*>(smem + sizeof(RowShared));
     // f(logit, id) for every token of the slice
     auto each = [&](auto f) {
-        if constexpr (REG) {
-#pragma unroll
-            for (int e = 0; e < kRegs; ++e) {
-                const int j = threadIdx.x + e * kThreads;
-                if (j < n) f(reg[e], lo + j);
-            }
-        } else {
 #pragma unroll 4
-            for (int j = threadIdx.x; j < n; j += kThreads) f(__ldg(row + j), lo + j);
-        }
+        for (int j = threadIdx.x; j < n; j += kThreads) f(KEPT ? kept[j] : __ldg(row + j), lo + j);
     };
 
-    // ---- the largest key of the row and its smallest finite logit
+    // ---- the largest logit of the row and its smallest finite one
     if (threadIdx.x < 64) sh.table[threadIdx.x] = exp2(-static_cast<double>(threadIdx.x) / 64.0);
     hist_clear(sh);
-    u64 best = 0;
-    float least = INFINITY;
-    each([&](float l, int id) {
-        const u64 key = row_key(l, id);
-        best = key > best ? key : best;
-        if (l > -INFINITY && l < least) least = l;
-    });
-    best = warp_max_u64(best);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) least = fminf(least, __shfl_xor_sync(0xffffffffu, least, o));
-    if (lane == 0) { sh.red_a[warp] = best; sh.red_f[warp] = least; }
+    if (threadIdx.x == 0) { sh.hit = 0; sh.bin = 0; }
+    float lmax = -INFINITY, least = INFINITY;
+#pragma unroll 8
+    for (int j = threadIdx.x; j < n; j += kThreads) {
+        const float l = __ldg(row + j);
+        if (KEPT) kept[j] = l;                 // read back by this thread only
+        lmax = fmaxf(lmax, l);                 // NaN never wins
+        if (l > -INFINITY) least = fminf(least, l);
+    }
+    lmax = warp_max(lmax);
+    least = -warp_max(-least);
+    if (lane == 0) { sh.red_f[warp] = lmax; sh.red_g[warp] = least; }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kWarps; ++w) {
-            best = sh.red_a[w] > best ? sh.red_a[w] : best;
-            least = fminf(least, sh.red_f[w]);
-        }
-        sh.x_max = best;
-        sh.x_min = least;
+    if (warp == 0) {
+        lmax = warp_max(lane < kWarps ? sh.red_f[lane] : -INFINITY);
+        least = -warp_max(lane < kWarps ? -sh.red_g[lane] : -INFINITY);
+        if (lane == 0) { sh.x_max = lmax; sh.x_min = least; }
     }
     cluster_sync();
-    {
-        u64 m = lane < kRanks ? ld_peer64(&sh.x_max, lane) : 0ull;
-        float f = lane < kRanks ? __uint_as_float(ld_peer32(&sh.x_min, lane)) : INFINITY;
-        best = warp_max_u64(m);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) f = fminf(f, __shfl_xor_sync(0xffffffffu, f, o));
-        least = f;
-    }
-    Scale sc;
-    sc.lmax = key_logit(best);
-    if (T == 0.f || sc.lmax == -INFINITY) {
-        if (rank == 0 && threadIdx.x == 0) out[b] = key_id(best);
+    lmax = warp_max(lane < kRanks ? __uint_as_float(ld_peer32(&sh.x_max, lane)) : -INFINITY);
+    least = -warp_max(lane < kRanks ? -__uint_as_float(ld_peer32(&sh.x_min, lane)) : -INFINITY);
+    if (T == 0.f || lmax == -INFINITY) {
+        // greedy: the lowest id at the maximum (a row without a finite logit: token 0)
+        int id0 = 0x7fffffff;
+        if (lmax > -INFINITY)
+            each([&](float l, int id) { if (l == lmax) id0 = min(id0, id); });
+        id0 = __reduce_min_sync(0xffffffffu, id0);
+        if (lane == 0) sh.red_b[warp] = static_cast<u64>(id0);
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            for (int w = 1; w < kWarps; ++w) id0 = min(id0, static_cast<int>(sh.red_b[w]));
+            sh.x_id = id0;
+        }
+        cluster_sync();
+        if (rank == 0 && warp == 0) {
+            id0 = lane < kRanks ? static_cast<int>(ld_peer32(&sh.x_id, lane)) : 0x7fffffff;
+            id0 = __reduce_min_sync(0xffffffffu, id0);
+            if (lane == 0) out[b] = id0 == 0x7fffffff ? 0 : id0;
+        }
         cluster_sync();                        // no CTA leaves while its shared memory may be read
         return;
     }
+    Scale sc;
+    sc.lmax = lmax;
     sc.c64 = 64.0 * 1.4426950408889634074 / static_cast<double>(T);
-    const float reach = fminf(kReach * T, sc.lmax - least);
+    // distances beyond `reach` weigh nothing; without top-k and top-p, neither
+    // do those that min-p drops (a little further, for its own exact test)
+    float reach = fminf(kReach * T, lmax - least);
+    if (k <= 0 && tp >= 1.f && mp > 0.f) reach = fminf(reach, (-logf(mp) * 1.0001f + 1e-4f) * T);
     sc.cbin = reach > 0.f ? static_cast<float>(kBins) / reach : 0.f;
     if (!(sc.cbin < INFINITY)) sc.cbin = 3e38f;
-
-    // ---- histogram of the row; its mass and min-p's
     const double mp46 = static_cast<double>(mp) * kFix;
-    u64 s = 0, zm = 0;
-    each([&](float l, int) {
-        bool keep;
-        const u64 m = row_mass(sh, sc, l, mp46, &keep);
-        if (m == 0) return;
-        s += m;
-        if (keep) zm += m;
-        hist_add(sh, row_bin(sc, l), m);
-    });
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        s += __shfl_xor_sync(0xffffffffu, s, o);
-        zm += __shfl_xor_sync(0xffffffffu, zm, o);
-    }
-    if (lane == 0) { sh.red_a[warp] = s; sh.red_b[warp] = zm; }
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kWarps; ++w) zm += sh.red_b[w];
-        sh.x_zm = zm;
-    }
-    hist_reduce(sh, sh.p0, rank);
-    s = sh.p0.mass[kBins];
-    {
-        u64 m = lane < kRanks ? ld_peer64(&sh.x_zm, lane) : 0ull;
-#pragma unroll
-        for (int o = 4; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
-        zm = __shfl_sync(0xffffffffu, m, 0);
-    }
+    // the tokens within reach (an infinite maximum is within reach of itself)
+    auto within = [&](float l) { return l == lmax || lmax - l <= reach; };
 
-    // ---- searches
-    int turn = 0;                              // list buffer of the next gather
-    int have_lo = 1, have_hi = 0;              // bins of the row's histogram the list holds
-    u64 list_mass = 0;                         // mass before the list
-    unsigned int list_cnt = 0;
+    // ---- lists
+    int turn = 0;                              // buffer of the next gather
     int list_n = 0;
-    // Gathers the tokens that `in` accepts (at most kCap over the cluster) into
-    // sh.key / sh.mass of every CTA.
-    auto gather = [&](auto in) {
+    // Gathers the tokens that `in` accepts (at most kCap over the cluster) and
+    // sorts them; `before` is the mass ahead of the list.
+    auto gather = [&](u64 before, auto in) {
         if (threadIdx.x == 0) sh.seg_n[turn] = 0;
         __syncthreads();
         each([&](float l, int id) {
-            const u64 key = row_key(l, id);
-            if (!in(l, key)) return;
+            if (!within(l) || !in(l, id)) return;
             bool keep;
-            const u64 m = row_mass(sh, sc, l, 0.0, &keep);
+            const u64 m = row_mass(sh, sc, l, mp46, &keep);
             if (m == 0) return;
             const int at = atomicAdd(&sh.seg_n[turn], 1);
-            sh.seg_key[turn][at] = key;
-            sh.seg_mass[turn][at] = m;
+            sh.seg_key[turn][at] = row_key(l, id);
+            sh.seg_mass[turn][at] = m | (keep ? kKeep : 0ull);
         });
         cluster_sync();
         const int mine = lane < kRanks ? static_cast<int>(ld_peer32(&sh.seg_n[turn], lane)) : 0;
@@ -368,33 +335,123 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         list_n = at;
         turn ^= 1;
         __syncthreads();
+        // rank and mass before of entry threadIdx.x / 2, half of the list in each of two threads
+        {
+            const int i = threadIdx.x >> 1, half = (list_n + 1) >> 1;
+            const int j0 = (threadIdx.x & 1) * half, j1 = min(list_n, j0 + half);
+            const u64 key = i < list_n ? sh.key[i] : ~0ull;
+            u64 bm = 0;
+            int rk = 0;
+            if (i < list_n) {
+#pragma unroll 4
+                for (int j = j0; j < j1; ++j) {
+                    const bool ahead = sh.key[j] > key;
+                    bm += ahead ? sh.mass[j] & ~kKeep : 0ull;
+                    rk += ahead;
+                }
+            }
+            bm += __shfl_xor_sync(0xffffffffu, bm, 1);
+            rk += __shfl_xor_sync(0xffffffffu, rk, 1);
+            if (i < list_n && (threadIdx.x & 1) == 0) {
+                const u64 m = sh.mass[i];
+                sh.s_key[rk] = key;
+                sh.s_pre[rk] = before + bm;
+                sh.s_keep[rk] = (m & kKeep) != 0;
+                if (rk == list_n - 1) sh.s_pre[list_n] = before + bm + (m & ~kKeep);
+            }
+        }
+        __syncthreads();
     };
-    // The first token whose inclusive mass (by_count: count) exceeds `target`
-    // (there is one): its key, mass and the mass before it in sh.res_*.
+    // Index in the list of the first token whose inclusive mass exceeds `target`.
+    auto hit_of = [&](u64 target) {
+        for (int i = threadIdx.x; i < list_n; i += kThreads)
+            if (sh.s_pre[i] <= target && target < sh.s_pre[i + 1]) sh.hit = i;
+        __syncthreads();
+        const int i = sh.hit;
+        __syncthreads();
+        return i;
+    };
+    // u below 1, so that the target stays below the kept mass
+    const double u = fmin(fmax(static_cast<double>(uniforms[b]), 0.0), 1.0 - 1.0 / 16777216.0);
+    auto finish = [&](int i) {
+        if (rank == 0 && threadIdx.x == 0) out[b] = key_id(sh.s_key[i]);
+        cluster_sync();                        // no CTA leaves while its shared memory may be read
+    };
+
+    // ---- a small top_k: counts, one list with every token that may be drawn
+    if (k > 0 && k <= kCap) {
+        each([&](float l, int) { if (within(l)) atomicAdd(&sh.h[0][row_bin(sc, l)], 1u); });
+        hist_reduce<false>(sh, sh.p0, rank);
+        const unsigned int all = sh.p0.cnt[kBins];
+        const int bin = choose_bin(sh, sh.p0, true, min(static_cast<unsigned int>(k), all) - 1);
+        if (sh.p0.cnt[bin + 1] <= kCap) {
+            gather(0, [&](float l, int) { return row_bin(sc, l) <= bin; });
+            u64 z = sh.s_pre[min(k, list_n)];
+            if (tp < 1.f) {
+                const u64 zp = sh.s_pre[hit_of(static_cast<u64>(static_cast<double>(tp) * static_cast<double>(z))) + 1];
+                z = zp < z ? zp : z;
+            }
+            if (mp > 0.f) {
+                for (int i = threadIdx.x; i < list_n; i += kThreads)
+                    if (sh.s_keep[i] && (i + 1 == list_n || !sh.s_keep[i + 1])) sh.hit = i;
+                __syncthreads();
+                const u64 zm = sh.s_pre[sh.hit + 1];
+                z = zm < z ? zm : z;
+                __syncthreads();
+            }
+            finish(hit_of(static_cast<u64>(u * static_cast<double>(z))));
+            return;
+        }
+        hist_clear(sh);                        // its last readers passed the sums' second barrier
+        __syncthreads();
+    }
+
+    // ---- histogram of masses; the row's mass and min-p's
+    u64 zm = 0;
+    each([&](float l, int) {
+        if (!within(l)) return;
+        bool keep;
+        const u64 m = row_mass(sh, sc, l, mp46, &keep);
+        if (m == 0) return;
+        if (keep) zm += m;
+        hist_add(sh, row_bin(sc, l), m);
+    });
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) zm += __shfl_xor_sync(0xffffffffu, zm, o);
+    if (lane == 0) sh.red_b[warp] = zm;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        for (int w = 1; w < kWarps; ++w) zm += sh.red_b[w];
+        sh.x_zm = zm;
+    }
+    hist_reduce<true>(sh, sh.p0, rank);
+    {
+        u64 m = lane < kRanks ? ld_peer64(&sh.x_zm, lane) : 0ull;
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+        zm = __shfl_sync(0xffffffffu, m, 0);
+    }
+    int have_lo = 1, have_hi = 0;              // bins that the list holds whole
+    unsigned int list_cnt = 0;                 // tokens before the list
+    // Index in the list of the first token whose inclusive mass (by_count: count)
+    // exceeds `target`; there is one.
     auto find = [&](bool by_count, u64 target) {
         const int bin = choose_bin(sh, sh.p0, by_count, target);
         if (bin < have_lo || bin > have_hi) {
-            const unsigned int upto = sh.p0.cnt[bin + 1], within = upto - sh.p0.cnt[bin];
-            if (upto <= kCap) {
-                have_lo = 0;
+            const unsigned int upto = sh.p0.cnt[bin + 1], inside0 = upto - sh.p0.cnt[bin];
+            if (inside0 <= kCap) {
+                have_lo = upto <= kCap ? 0 : bin;
                 have_hi = bin;
-                gather([&](float l, u64) { return row_bin(sc, l) <= bin; });
-            } else if (within <= kCap) {
-                have_lo = have_hi = bin;
-                gather([&](float l, u64) { return row_bin(sc, l) == bin; });
+                list_cnt = sh.p0.cnt[have_lo];
+                gather(sh.p0.mass[have_lo], [&](float l, int) { const int x = row_bin(sc, l); return x >= have_lo && x <= bin; });
             } else {
                 have_lo = 1;                   // a list of part of a bin serves no other search
                 have_hi = 0;
-            }
-            if (have_lo <= have_hi) {
-                list_mass = sh.p0.mass[have_lo];
-                list_cnt = sh.p0.cnt[have_lo];
-            } else {
                 // cut the bin by its order keys [k0, k1]
                 u64 k1 = 0, k0 = ~0ull;
                 each([&](float l, int id) {
                     bool keep;
-                    if (row_bin(sc, l) != bin || row_mass(sh, sc, l, 0.0, &keep) == 0) return;
+                    if (!within(l) || row_bin(sc, l) != bin || row_mass(sh, sc, l, mp46, &keep) == 0) return;
                     const u64 key = row_key(l, id);
                     k1 = key > k1 ? key : k1;
                     k0 = key < k0 ? key : k0;
@@ -408,15 +465,15 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
                         k1 = sh.red_a[w] > k1 ? sh.red_a[w] : k1;
                         k0 = sh.red_b[w] < k0 ? sh.red_b[w] : k0;
                     }
-                    sh.x_max = k1;
-                    sh.x_s = k0;
+                    sh.x_k1 = k1;
+                    sh.x_k0 = k0;
                 }
                 cluster_sync();
-                k1 = warp_max_u64(lane < kRanks ? ld_peer64(&sh.x_max, lane) : 0ull);
-                k0 = ~warp_max_u64(lane < kRanks ? ~ld_peer64(&sh.x_s, lane) : 0ull);
-                list_mass = sh.p0.mass[bin];
+                k1 = warp_max_u64(lane < kRanks ? ld_peer64(&sh.x_k1, lane) : 0ull);
+                k0 = ~warp_max_u64(lane < kRanks ? ~ld_peer64(&sh.x_k0, lane) : 0ull);
+                u64 before = sh.p0.mass[bin];
                 list_cnt = sh.p0.cnt[bin];
-                unsigned int inside = within;
+                unsigned int inside = inside0;
                 while (inside > kCap) {
                     const int bits = 64 - __clzll(static_cast<long long>(k1 - k0));
                     const int shift = bits > 10 ? bits - 10 : 0;
@@ -427,12 +484,12 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
                         const u64 key = row_key(l, id);
                         if (key < k0 || key > k1) return;
                         bool keep;
-                        const u64 m = row_mass(sh, sc, l, 0.0, &keep);
+                        const u64 m = row_mass(sh, sc, l, mp46, &keep);
                         if (m) hist_add(sh, static_cast<int>((k1 - key) >> shift), m);
                     });
-                    hist_reduce(sh, sh.p1, rank);
-                    const int cut = choose_bin(sh, sh.p1, by_count, target - (by_count ? list_cnt : list_mass));
-                    list_mass += sh.p1.mass[cut];
+                    hist_reduce<true>(sh, sh.p1, rank);
+                    const int cut = choose_bin(sh, sh.p1, by_count, target - (by_count ? list_cnt : before));
+                    before += sh.p1.mass[cut];
                     list_cnt += sh.p1.cnt[cut];
                     inside = sh.p1.cnt[cut + 1] - sh.p1.cnt[cut];
                     const u64 top = k1 - (static_cast<u64>(cut) << shift);
@@ -440,70 +497,44 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
                     k0 = low > k0 && low <= top ? low : k0;
                     k1 = top;
                 }
-                gather([&](float, u64 key) { return key >= k0 && key <= k1; });
+                gather(before, [&](float l, int id) { const u64 key = row_key(l, id); return key >= k0 && key <= k1; });
             }
         }
-        // place the token in the list: what lies before it in the list
-        for (int i = threadIdx.x; i < list_n; i += kThreads) {
-            const u64 key = sh.key[i], m = sh.mass[i];
-            u64 bm = list_mass;
-            unsigned int bc = list_cnt;
-            for (int j = 0; j < list_n; ++j) {
-                const bool ahead = sh.key[j] > key;
-                bm += ahead ? sh.mass[j] : 0ull;
-                bc += ahead;
-            }
-            if (by_count ? bc == target : bm <= target && target < bm + m) {
-                sh.res_before = bm;
-                sh.res_key = key;
-                sh.res_mass = m;
-            }
-        }
-        __syncthreads();
+        return by_count ? static_cast<int>(target - list_cnt) : hit_of(target);
     };
+    const u64 s = sh.p0.mass[kBins];
     u64 z = s;
-    if (k > 0 && static_cast<unsigned int>(k) < sh.p0.cnt[kBins]) {
-        find(true, static_cast<u64>(k - 1));
-        z = sh.res_before + sh.res_mass;
-        __syncthreads();
-    }
+    if (k > 0 && static_cast<unsigned int>(k) < sh.p0.cnt[kBins]) z = sh.s_pre[find(true, static_cast<u64>(k - 1)) + 1];
     if (tp < 1.f) {
         const u64 target = static_cast<u64>(static_cast<double>(tp) * static_cast<double>(z));
-        if (target < s) {                      // the edge; never short of the first token
-            find(false, target);
-            const u64 zp = sh.res_before + sh.res_mass;
+        if (target < s) {
+            const u64 zp = sh.s_pre[find(false, target) + 1];
             z = zp < z ? zp : z;
-            __syncthreads();
         }
     }
     z = zm < z ? zm : z;
-    // u below 1, so the target stays below the kept mass
-    const double u = fmin(fmax(static_cast<double>(uniforms[b]), 0.0), 1.0 - 1.0 / 16777216.0);
-    find(false, static_cast<u64>(u * static_cast<double>(z)));
-    if (rank == 0 && threadIdx.x == 0) out[b] = key_id(sh.res_key);
-    cluster_sync();                            // no CTA leaves while its shared memory may be read
+    __syncthreads();
+    finish(find(false, static_cast<u64>(u * static_cast<double>(z))));
 }
 
-template <bool REG>
+template <bool KEPT>
 static int rows_go(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
                    const float* top_p, const float* min_p, const float* uniforms, int32_t* out, cudaStream_t st) {
+    constexpr int smem = static_cast<int>(sizeof(RowShared)) + (KEPT ? kKept * 4 : 0);
     static bool attr = false;
     if (!attr) {
-        cudaError_t e = cudaFuncSetAttribute(sample_rows_kernel<REG>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             static_cast<int>(sizeof(RowShared)));
+        cudaError_t e = cudaFuncSetAttribute(sample_rows_kernel<KEPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(sample_rows_kernel)");
         attr = true;
     }
-    sample_rows_kernel<REG><<<B * kRanks, kThreads, sizeof(RowShared), st>>>(logits, V, temperature, top_k, top_p, min_p,
-                                                                           uniforms, out);
+    sample_rows_kernel<KEPT><<<B * kRanks, kThreads, smem, st>>>(logits, V, temperature, top_k, top_p, min_p, uniforms, out);
     LLB_CHECK_LAUNCH("sample_rows_kernel");
     return LLAMA_OK;
 }
 
 int launch_sample_rows(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
                        const float* top_p, const float* min_p, const float* uniforms, int32_t* out, cudaStream_t st) {
-    if (V <= kRanks * kThreads * kRegs)
-        return rows_go<true>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
+    if (V <= kRanks * kKept) return rows_go<true>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
     return rows_go<false>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
 }
 
