@@ -219,7 +219,7 @@ __device__ __forceinline__ int choose_bin(RowShared& sh, const Prefix& p, bool b
 // KEPT: the CTA's slice of the row stays in shared memory (V <= 32768);
 // otherwise each pass reads it again (from L2).
 template <bool KEPT>
-__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads)
+__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads, 2)
 sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restrict__ temperature,
                    const int32_t* __restrict__ top_k, const float* __restrict__ top_p,
                    const float* __restrict__ min_p, const float* __restrict__ uniforms, int32_t* __restrict__ out) {
@@ -239,11 +239,41 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     const int S = (V + kRanks - 1) / kRanks, lo = static_cast<int>(rank) * S;
     const int n = max(0, min(S, V - lo));
     const float* row = logits + static_cast<long long>(b) * V + lo;
-    float* kept = reinterpret_cast<float*>(smem + sizeof(RowShared));
-    // f(logit, id) for every token of the slice
+    // The slice as 16-byte vectors of aligned addresses; its first and last may
+    // reach outside the slice, where values read as -inf and are skipped.
+    const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 2) & 3);
+    const int nv = n > 0 ? (n + mis + 3) >> 2 : 0;
+    float4* kept = reinterpret_cast<float4*>(smem + sizeof(RowShared));
+    constexpr int kBatch = KEPT ? 2 : 4;       // vectors a thread has in flight
+    auto fetch = [&](int i) {
+        const int j = 4 * i - mis;
+        if (j >= 0 && j + 4 <= n) return __ldg(reinterpret_cast<const float4*>(row + j));
+        float4 v;
+        v.x = j >= 0 ? __ldg(row + j) : -INFINITY;
+        v.y = j + 1 >= 0 && j + 1 < n ? __ldg(row + j + 1) : -INFINITY;
+        v.z = j + 2 >= 0 && j + 2 < n ? __ldg(row + j + 2) : -INFINITY;
+        v.w = j + 3 < n ? __ldg(row + j + 3) : -INFINITY;
+        return v;
+    };
+    // f(logit, id) for every token of the slice, four vectors in flight
     auto each = [&](auto f) {
-#pragma unroll 4
-        for (int j = threadIdx.x; j < n; j += kThreads) f(KEPT ? kept[j] : __ldg(row + j), lo + j);
+        for (int i0 = threadIdx.x; i0 < nv; i0 += kBatch * kThreads) {
+            float4 v[kBatch];
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+                const int i = i0 + x * kThreads;
+                if (i < nv) v[x] = KEPT ? kept[i] : fetch(i);
+            }
+#pragma unroll
+            for (int x = 0; x < kBatch; ++x) {
+                const int i = i0 + x * kThreads, j = 4 * i - mis;
+                if (i >= nv) break;
+                if (j >= 0) f(v[x].x, lo + j);
+                if (j + 1 >= 0 && j + 1 < n) f(v[x].y, lo + j + 1);
+                if (j + 2 >= 0 && j + 2 < n) f(v[x].z, lo + j + 2);
+                if (j + 3 < n) f(v[x].w, lo + j + 3);
+            }
+        }
     };
 
     // ---- the largest logit of the row and its smallest finite one
@@ -251,12 +281,23 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     hist_clear(sh);
     if (threadIdx.x == 0) { sh.hit = 0; sh.bin = 0; }
     float lmax = -INFINITY, least = INFINITY;
-#pragma unroll 8
-    for (int j = threadIdx.x; j < n; j += kThreads) {
-        const float l = __ldg(row + j);
-        if (KEPT) kept[j] = l;                 // read back by this thread only
-        lmax = fmaxf(lmax, l);                 // NaN never wins
-        if (l > -INFINITY) least = fminf(least, l);
+    for (int i0 = threadIdx.x; i0 < nv; i0 += kBatch * kThreads) {
+        float4 v[kBatch];
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            const int i = i0 + x * kThreads;
+            v[x] = i < nv ? fetch(i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            if (KEPT && i < nv) kept[i] = v[x];                // read back by this thread only
+        }
+#pragma unroll
+        for (int x = 0; x < kBatch; ++x) {
+            const float l[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                lmax = fmaxf(lmax, l[y]);                      // NaN never wins
+                if (l[y] > -INFINITY) least = fminf(least, l[y]);
+            }
+        }
     }
     lmax = warp_max(lmax);
     least = -warp_max(-least);
@@ -520,7 +561,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
 template <bool KEPT>
 static int rows_go(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
                    const float* top_p, const float* min_p, const float* uniforms, int32_t* out, cudaStream_t st) {
-    constexpr int smem = static_cast<int>(sizeof(RowShared)) + (KEPT ? kKept * 4 : 0);
+    constexpr int smem = static_cast<int>(sizeof(RowShared)) + (KEPT ? (kKept + 4) * 4 : 0);
     static bool attr = false;
     if (!attr) {
         cudaError_t e = cudaFuncSetAttribute(sample_rows_kernel<KEPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
