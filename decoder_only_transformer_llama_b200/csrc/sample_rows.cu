@@ -22,8 +22,8 @@
 // and resolves alike.  A row with a small top_k needs counts only: its list
 // holds every token that may be drawn, and only their exponentials are taken.
 // Other rows add masses to the histogram.  A bin with more tokens than a list
-// holds (ties, flat rows) is cut by histograms over 1024 steps of the order key,
-// 10 bits of it at a time.
+// holds is cut into 1024 steps by a second histogram; a step with more (ties)
+// by histograms over the order key, 10 bits of it at a time.
 #include "common.cuh"
 #include "paged.h"
 
@@ -93,15 +93,18 @@ __device__ __forceinline__ void st_peer32(const void* p, uint32_t rank, unsigned
 
 // One row's scales.  e = 2^(-y / 64), y = (l_max - l) * c64 with c64 = 64 log2(e) / T.
 struct Scale {
-    float lmax;
-    double c64;
-    float cbin;        // bins per unit of l_max - l
+    float lmax, reach;   // distances beyond `reach` weigh nothing
+    double dmax, c64;    // l_max (0 if infinite)
+    float cbin;          // bins per unit of l_max - l
 };
 
-// e * 2^46 for a finite distance below the maximum: y = n + r, |r| <= 1/2, is cut into
-// n = 64 q + j, and 2^(-y/64) = 2^-q * 2^(-j/64) * exp(-r ln2 / 64) with the
-// exponential's Taylor terms up to the fifth power (|r ln2 / 64| < 0.0055: the
-// rest is below 4e-17).  Table-driven exponentials after Tang (1989).
+// Tokens that may weigh something (the equals of an infinite maximum too; never NaN or -inf).
+__device__ __forceinline__ bool within(const Scale& s, float l) { return l == s.lmax || s.lmax - l <= s.reach; }
+
+// e * 2^46 at y >= 0 below 68000: y = n + r, |r| <= 1/2, is cut into n = 64 q + j, and
+// 2^(-y/64) = 2^-q * 2^(-j/64) * exp(-r ln2 / 64) with the exponential's Taylor
+// terms up to the fifth power (|r ln2 / 64| < 0.0055: the rest is below 4e-17).
+// Table-driven exponentials after Tang (1989).
 __device__ __forceinline__ double scaled_exp(const RowShared& sh, double y) {
     constexpr double kMagic = 6755399441055744.0;              // 1.5 * 2^52: adding it rounds to an integer
     const double t = y + kMagic;
@@ -115,26 +118,26 @@ __device__ __forceinline__ double scaled_exp(const RowShared& sh, double y) {
     const double s = __longlong_as_double(static_cast<long long>(1023 + 46 - (n >> 6)) << 52);
     return sh.table[n & 63] * p * s;
 }
-// The mass of a logit, and whether min-p keeps it (e >= mp).
+// The mass of a logit (0 out of reach), and whether min-p keeps it (e >= mp).
+// Without branches: four of them overlap.
 __device__ __forceinline__ u64 row_mass(const RowShared& sh, const Scale& s, float l, double mp46, bool* keep) {
-    *keep = false;
-    if (!(l == l) || l == -INFINITY) return 0;
-    double e;
-    if (l == s.lmax) {
-        e = kFix;
-    } else {
-        const double y = (static_cast<double>(s.lmax) - static_cast<double>(l)) * s.c64;
-        if (!(y < 48.0 * 64.0)) { *keep = mp46 <= 0.0; return 0; }     // an infinite maximum too
-        e = scaled_exp(sh, y);
-    }
+    const bool in = within(s, l);
+    const double d = in && l != s.lmax ? s.dmax - static_cast<double>(l) : 0.0;
+    const double e = scaled_exp(sh, d * s.c64);
     *keep = e >= mp46;
-    return static_cast<u64>(__double_as_longlong(e + 4503599627370496.0) & 0xfffffffffffffLL);   // + 2^52: rounds
+    const u64 m = static_cast<u64>(__double_as_longlong(e + 4503599627370496.0) & 0xfffffffffffffLL);   // + 2^52: rounds
+    return in ? m : 0ull;
 }
 __device__ __forceinline__ int row_bin(const Scale& s, float l) {
-    const float d = s.lmax - l;
-    if (!(d > 0.f)) return 0;                  // the maximum itself (infinite ones too)
-    const float y = d * s.cbin;
-    return y < static_cast<float>(kBins - 1) ? static_cast<int>(y) : kBins - 1;
+    const float y = l == s.lmax ? 0.f : (s.lmax - l) * s.cbin;
+    return min(static_cast<int>(y), kBins - 1);
+}
+
+// The step within its bin, of 1024 (the bin number takes at most 10 bits of the
+// product's 24, so the steps are ordered like the tokens too).
+__device__ __forceinline__ int row_step(const Scale& s, float l) {
+    const float y = l == s.lmax ? 0.f : (s.lmax - l) * s.cbin;
+    return min(static_cast<int>((y - static_cast<float>(min(static_cast<int>(y), kBins - 1))) * kBins), kBins - 1);
 }
 
 // Adds a token to this CTA's histogram.
@@ -255,8 +258,8 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         v.w = j + 3 < n ? __ldg(row + j + 3) : -INFINITY;
         return v;
     };
-    // f(logit, id) for every token of the slice, four vectors in flight
-    auto each = [&](auto f) {
+    // f(four logits, first id) for every vector of the slice (-inf outside it)
+    auto each4 = [&](auto f) {
         for (int i0 = threadIdx.x; i0 < nv; i0 += kBatch * kThreads) {
             float4 v[kBatch];
 #pragma unroll
@@ -266,14 +269,44 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
             }
 #pragma unroll
             for (int x = 0; x < kBatch; ++x) {
-                const int i = i0 + x * kThreads, j = 4 * i - mis;
+                const int i = i0 + x * kThreads;
                 if (i >= nv) break;
-                if (j >= 0) f(v[x].x, lo + j);
-                if (j + 1 >= 0 && j + 1 < n) f(v[x].y, lo + j + 1);
-                if (j + 2 >= 0 && j + 2 < n) f(v[x].z, lo + j + 2);
-                if (j + 3 < n) f(v[x].w, lo + j + 3);
+                const float l[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+                f(l, lo + 4 * i - mis);
             }
         }
+    };
+    // f(logit, id) for the tokens that `in` accepts
+    auto each_of = [&](auto in, auto f) {
+        each4([&](const float (&l)[4], int id) {
+            bool t[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) t[y] = in(l[y], id + y);
+            if (t[0] || t[1] || t[2] || t[3]) {
+#pragma unroll 1
+                for (int y = 0; y < 4; ++y)
+                    if (in(l[y], id + y)) f(l[y], id + y);
+            }
+        });
+    };
+    // every token's mass to the histogram, at the bin that bin(logit, id) names (below 0: not at all)
+    auto fill = [&](const Scale& sc, double mp46, auto bin, u64* kept_mass) {
+        u64 zm = 0;
+        each4([&](const float (&l)[4], int id) {
+            u64 m[4];
+            int at[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+                bool keep;
+                m[y] = row_mass(sh, sc, l[y], mp46, &keep);
+                zm += keep ? m[y] : 0ull;
+                at[y] = bin(l[y], id + y);
+            }
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (m[y] != 0 && at[y] >= 0) hist_add(sh, at[y], m[y]);
+        });
+        *kept_mass = zm;
     };
 
     // ---- the largest logit of the row and its smallest finite one
@@ -315,7 +348,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         // greedy: the lowest id at the maximum (a row without a finite logit: token 0)
         int id0 = 0x7fffffff;
         if (lmax > -INFINITY)
-            each([&](float l, int id) { if (l == lmax) id0 = min(id0, id); });
+            each_of([&](float l, int) { return l == lmax; }, [&](float, int id) { id0 = min(id0, id); });
         id0 = __reduce_min_sync(0xffffffffu, id0);
         if (lane == 0) sh.red_b[warp] = static_cast<u64>(id0);
         __syncthreads();
@@ -339,11 +372,12 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     // do those that min-p drops (a little further, for its own exact test)
     float reach = fminf(kReach * T, lmax - least);
     if (k <= 0 && tp >= 1.f && mp > 0.f) reach = fminf(reach, (-logf(mp) * 1.0001f + 1e-4f) * T);
+    if (lmax == INFINITY) reach = 0.f;         // only its equals weigh anything
+    sc.reach = reach;
+    sc.dmax = lmax == INFINITY ? 0.0 : static_cast<double>(lmax);
     sc.cbin = reach > 0.f ? static_cast<float>(kBins) / reach : 0.f;
     if (!(sc.cbin < INFINITY)) sc.cbin = 3e38f;
     const double mp46 = static_cast<double>(mp) * kFix;
-    // the tokens within reach (an infinite maximum is within reach of itself)
-    auto within = [&](float l) { return l == lmax || lmax - l <= reach; };
 
     // ---- lists
     int turn = 0;                              // buffer of the next gather
@@ -353,8 +387,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     auto gather = [&](u64 before, auto in) {
         if (threadIdx.x == 0) sh.seg_n[turn] = 0;
         __syncthreads();
-        each([&](float l, int id) {
-            if (!within(l) || !in(l, id)) return;
+        each_of([&](float l, int id) { return within(sc, l) && in(l, id); }, [&](float l, int id) {
             bool keep;
             const u64 m = row_mass(sh, sc, l, mp46, &keep);
             if (m == 0) return;
@@ -363,17 +396,22 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
             sh.seg_mass[turn][at] = m | (keep ? kKeep : 0ull);
         });
         cluster_sync();
-        const int mine = lane < kRanks ? static_cast<int>(ld_peer32(&sh.seg_n[turn], lane)) : 0;
-        int at = 0;
-        for (uint32_t r = 0; r < kRanks; ++r) {
-            const int c = __shfl_sync(0xffffffffu, mine, r);
-            for (int i = threadIdx.x; i < c; i += kThreads) {
-                sh.key[at + i] = ld_peer64(&sh.seg_key[turn][i], r);
-                sh.mass[at + i] = ld_peer64(&sh.seg_mass[turn][i], r);
-            }
-            at += c;
+        // warp r copies CTA r's tokens
+        int at = lane < kRanks ? static_cast<int>(ld_peer32(&sh.seg_n[turn], lane)) : 0;
+        const int mine = __shfl_sync(0xffffffffu, at, warp & (kRanks - 1));
+#pragma unroll
+        for (int o = 1; o < kRanks; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, at, o);
+            if (lane >= o) at += y;
         }
-        list_n = at;
+        list_n = __shfl_sync(0xffffffffu, at, kRanks - 1);
+        at = __shfl_sync(0xffffffffu, at, warp & (kRanks - 1)) - mine;
+        if (warp < kRanks)
+            for (int i = lane; i < mine; i += 32) {
+                const u64 key = ld_peer64(&sh.seg_key[turn][i], warp), m = ld_peer64(&sh.seg_mass[turn][i], warp);
+                sh.key[at + i] = key;
+                sh.mass[at + i] = m;
+            }
         turn ^= 1;
         __syncthreads();
         // rank and mass before of entry threadIdx.x / 2, half of the list in each of two threads
@@ -421,7 +459,14 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
 
     // ---- a small top_k: counts, one list with every token that may be drawn
     if (k > 0 && k <= kCap) {
-        each([&](float l, int) { if (within(l)) atomicAdd(&sh.h[0][row_bin(sc, l)], 1u); });
+        each4([&](const float (&l)[4], int) {
+            int at[4];
+#pragma unroll
+            for (int y = 0; y < 4; ++y) at[y] = within(sc, l[y]) ? row_bin(sc, l[y]) : -1;
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (at[y] >= 0) atomicAdd(&sh.h[0][at[y]], 1u);
+        });
         hist_reduce<false>(sh, sh.p0, rank);
         const unsigned int all = sh.p0.cnt[kBins];
         const int bin = choose_bin(sh, sh.p0, true, min(static_cast<unsigned int>(k), all) - 1);
@@ -448,15 +493,8 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     }
 
     // ---- histogram of masses; the row's mass and min-p's
-    u64 zm = 0;
-    each([&](float l, int) {
-        if (!within(l)) return;
-        bool keep;
-        const u64 m = row_mass(sh, sc, l, mp46, &keep);
-        if (m == 0) return;
-        if (keep) zm += m;
-        hist_add(sh, row_bin(sc, l), m);
-    });
+    u64 zm;
+    fill(sc, mp46, [&](float l, int) { return row_bin(sc, l); }, &zm);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) zm += __shfl_xor_sync(0xffffffffu, zm, o);
     if (lane == 0) sh.red_b[warp] = zm;
@@ -488,11 +526,29 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
             } else {
                 have_lo = 1;                   // a list of part of a bin serves no other search
                 have_hi = 0;
-                // cut the bin by its order keys [k0, k1]
+                // cut the bin into 1024 steps of the distance
+                __syncthreads();
+                hist_clear(sh);
+                __syncthreads();
+                u64 unused;
+                fill(sc, mp46, [&](float l, int) { return row_bin(sc, l) == bin ? row_step(sc, l) : -1; }, &unused);
+                hist_reduce<true>(sh, sh.p1, rank);
+                u64 before = sh.p0.mass[bin];
+                list_cnt = sh.p0.cnt[bin];
+                const int step = choose_bin(sh, sh.p1, by_count, target - (by_count ? list_cnt : before));
+                before += sh.p1.mass[step];
+                list_cnt += sh.p1.cnt[step];
+                unsigned int inside = sh.p1.cnt[step + 1] - sh.p1.cnt[step];
+                auto in_step = [&](float l, int) { return within(sc, l) && row_bin(sc, l) == bin && row_step(sc, l) == step; };
+                if (inside <= kCap) {
+                    gather(before, in_step);
+                    return by_count ? static_cast<int>(target - list_cnt) : hit_of(target);
+                }
+                // near ties: cut the step by its order keys [k0, k1]
                 u64 k1 = 0, k0 = ~0ull;
-                each([&](float l, int id) {
+                each_of(in_step, [&](float l, int id) {
                     bool keep;
-                    if (!within(l) || row_bin(sc, l) != bin || row_mass(sh, sc, l, mp46, &keep) == 0) return;
+                    if (row_mass(sh, sc, l, mp46, &keep) == 0) return;
                     const u64 key = row_key(l, id);
                     k1 = key > k1 ? key : k1;
                     k0 = key < k0 ? key : k0;
@@ -512,22 +568,16 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
                 cluster_sync();
                 k1 = warp_max_u64(lane < kRanks ? ld_peer64(&sh.x_k1, lane) : 0ull);
                 k0 = ~warp_max_u64(lane < kRanks ? ~ld_peer64(&sh.x_k0, lane) : 0ull);
-                u64 before = sh.p0.mass[bin];
-                list_cnt = sh.p0.cnt[bin];
-                unsigned int inside = inside0;
                 while (inside > kCap) {
                     const int bits = 64 - __clzll(static_cast<long long>(k1 - k0));
                     const int shift = bits > 10 ? bits - 10 : 0;
                     __syncthreads();
                     hist_clear(sh);
                     __syncthreads();
-                    each([&](float l, int id) {
+                    fill(sc, mp46, [&](float l, int id) {
                         const u64 key = row_key(l, id);
-                        if (key < k0 || key > k1) return;
-                        bool keep;
-                        const u64 m = row_mass(sh, sc, l, mp46, &keep);
-                        if (m) hist_add(sh, static_cast<int>((k1 - key) >> shift), m);
-                    });
+                        return key >= k0 && key <= k1 ? static_cast<int>((k1 - key) >> shift) : -1;
+                    }, &unused);
                     hist_reduce<true>(sh, sh.p1, rank);
                     const int cut = choose_bin(sh, sh.p1, by_count, target - (by_count ? list_cnt : before));
                     before += sh.p1.mass[cut];
