@@ -14,7 +14,7 @@
 // 64-bit fixed point (2^-46 resolution): every prefix sum is an exact integer
 // in any order, and tokens below 2^-47 of the maximum weigh nothing.
 //
-// A row is spread over a cluster of 8 CTAs.  A histogram over 1024 equal steps
+// A row is spread over a cluster of R = 8, 4 or 2 CTAs.  A histogram over 1024 equal steps
 // of l_max - l (bins are ordered like the tokens), summed over the cluster
 // through distributed shared memory, turns each of the three searches (k-th
 // token, nucleus edge, draw) into the choice of a bin; the tokens up to that
@@ -32,12 +32,11 @@ namespace llb {
 namespace {
 typedef unsigned long long u64;
 
-constexpr int kRanks = 8;
 constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kCap = 256;                     // tokens one list holds
-constexpr int kKept = 4096;                   // logits of a slice that stay in shared memory (V <= 32768)
+constexpr int kKept = 8192;                   // logits of a slice that stay in shared memory
 constexpr double kFix = 70368744177664.0;     // 2^46: V * 2^46 < 2^64 for V <= 262144
 constexpr u64 kKeep = 1ull << 63;             // beside a mass: min-p keeps the token
 constexpr float kReach = 32.625f;             // 47 ln 2 = 32.58: masses beyond round to 0
@@ -152,12 +151,12 @@ __device__ __forceinline__ void hist_clear(RowShared& sh) {
 }
 
 // The cluster's totals of the histograms, as sums before each bin, into `p` of every CTA.
-template <bool MASS>
-__device__ void hist_reduce(RowShared& sh, Prefix& p, uint32_t rank) {
+template <int R, bool MASS>
+__device__ __forceinline__ void hist_reduce(RowShared& sh, Prefix& p, uint32_t rank) {
     cluster_sync();
     {
-        // CTA r adds up bins [128 r, 128 r + 128): four threads a bin, two CTAs each
-        const int bin = static_cast<int>(rank) * (kBins / kRanks) + (threadIdx.x >> 2), q = threadIdx.x & 3;
+        // CTA r adds up its share of the bins: R / 2 threads a bin, two CTAs each
+        const int bin = static_cast<int>(rank) * (kBins / R) + threadIdx.x / (R / 2), q = threadIdx.x % (R / 2);
         u64 m = 0;
         unsigned int c = 0;
 #pragma unroll
@@ -169,7 +168,7 @@ __device__ void hist_reduce(RowShared& sh, Prefix& p, uint32_t rank) {
                      (static_cast<u64>(ld_peer32(&sh.h[3][bin], from)) << 32);
         }
 #pragma unroll
-        for (int o = 1; o < 4; o <<= 1) {
+        for (int o = 1; o < R / 2; o <<= 1) {
             m += __shfl_xor_sync(0xffffffffu, m, o);
             c += __shfl_xor_sync(0xffffffffu, c, o);
         }
@@ -219,17 +218,17 @@ __device__ __forceinline__ int choose_bin(RowShared& sh, const Prefix& p, bool b
 }
 }  // namespace
 
-// KEPT: the CTA's slice of the row stays in shared memory (V <= 32768);
+// KEPT: the CTA's slice of the row stays in shared memory (up to 8192 logits);
 // otherwise each pass reads it again (from L2).
-template <bool KEPT>
-__global__ void __cluster_dims__(kRanks, 1, 1) __launch_bounds__(kThreads, 2)
+template <int R, bool KEPT>
+__global__ void __launch_bounds__(kThreads, 2)
 sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restrict__ temperature,
                    const int32_t* __restrict__ top_k, const float* __restrict__ top_p,
                    const float* __restrict__ min_p, const float* __restrict__ uniforms, int32_t* __restrict__ out) {
     extern __shared__ __align__(16) uint8_t smem[];
     RowShared& sh = *reinterpret_cast<RowShared*>(smem);
     const uint32_t rank = cluster_rank();
-    const int b = blockIdx.x / kRanks;
+    const int b = blockIdx.x / R;
     const float T = temperature[b];
     const int k = top_k ? top_k[b] : 0;
     const float tp = top_p ? top_p[b] : 1.f;
@@ -239,7 +238,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         return;                                // the whole cluster, before any exchange
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int S = (V + kRanks - 1) / kRanks, lo = static_cast<int>(rank) * S;
+    const int S = (V + R - 1) / R, lo = static_cast<int>(rank) * S;
     const int n = max(0, min(S, V - lo));
     const float* row = logits + static_cast<long long>(b) * V + lo;
     // The slice as 16-byte vectors of aligned addresses; its first and last may
@@ -259,7 +258,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         return v;
     };
     // f(four logits, first id) for every vector of the slice (-inf outside it)
-    auto each4 = [&](auto f) {
+    auto each4 = [&](auto f) __attribute__((always_inline)) {
         for (int i0 = threadIdx.x; i0 < nv; i0 += kBatch * kThreads) {
             float4 v[kBatch];
 #pragma unroll
@@ -277,7 +276,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         }
     };
     // f(logit, id) for the tokens that `in` accepts
-    auto each_of = [&](auto in, auto f) {
+    auto each_of = [&](auto in, auto f) __attribute__((always_inline)) {
         each4([&](const float (&l)[4], int id) {
             bool t[4];
 #pragma unroll
@@ -289,26 +288,6 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
             }
         });
     };
-    // every token's mass to the histogram, at the bin that bin(logit, id) names (below 0: not at all)
-    auto fill = [&](const Scale& sc, double mp46, auto bin, u64* kept_mass) {
-        u64 zm = 0;
-        each4([&](const float (&l)[4], int id) {
-            u64 m[4];
-            int at[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) {
-                bool keep;
-                m[y] = row_mass(sh, sc, l[y], mp46, &keep);
-                zm += keep ? m[y] : 0ull;
-                at[y] = bin(l[y], id + y);
-            }
-#pragma unroll
-            for (int y = 0; y < 4; ++y)
-                if (m[y] != 0 && at[y] >= 0) hist_add(sh, at[y], m[y]);
-        });
-        *kept_mass = zm;
-    };
-
     // ---- the largest logit of the row and its smallest finite one
     if (threadIdx.x < 64) sh.table[threadIdx.x] = exp2(-static_cast<double>(threadIdx.x) / 64.0);
     hist_clear(sh);
@@ -342,8 +321,8 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         if (lane == 0) { sh.x_max = lmax; sh.x_min = least; }
     }
     cluster_sync();
-    lmax = warp_max(lane < kRanks ? __uint_as_float(ld_peer32(&sh.x_max, lane)) : -INFINITY);
-    least = -warp_max(lane < kRanks ? -__uint_as_float(ld_peer32(&sh.x_min, lane)) : -INFINITY);
+    lmax = warp_max(lane < R ? __uint_as_float(ld_peer32(&sh.x_max, lane)) : -INFINITY);
+    least = -warp_max(lane < R ? -__uint_as_float(ld_peer32(&sh.x_min, lane)) : -INFINITY);
     if (T == 0.f || lmax == -INFINITY) {
         // greedy: the lowest id at the maximum (a row without a finite logit: token 0)
         int id0 = 0x7fffffff;
@@ -358,7 +337,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         }
         cluster_sync();
         if (rank == 0 && warp == 0) {
-            id0 = lane < kRanks ? static_cast<int>(ld_peer32(&sh.x_id, lane)) : 0x7fffffff;
+            id0 = lane < R ? static_cast<int>(ld_peer32(&sh.x_id, lane)) : 0x7fffffff;
             id0 = __reduce_min_sync(0xffffffffu, id0);
             if (lane == 0) out[b] = id0 == 0x7fffffff ? 0 : id0;
         }
@@ -384,7 +363,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     int list_n = 0;
     // Gathers the tokens that `in` accepts (at most kCap over the cluster) and
     // sorts them; `before` is the mass ahead of the list.
-    auto gather = [&](u64 before, auto in) {
+    auto gather = [&](u64 before, auto in) __attribute__((always_inline)) {
         if (threadIdx.x == 0) sh.seg_n[turn] = 0;
         __syncthreads();
         each_of([&](float l, int id) { return within(sc, l) && in(l, id); }, [&](float l, int id) {
@@ -397,16 +376,16 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         });
         cluster_sync();
         // warp r copies CTA r's tokens
-        int at = lane < kRanks ? static_cast<int>(ld_peer32(&sh.seg_n[turn], lane)) : 0;
-        const int mine = __shfl_sync(0xffffffffu, at, warp & (kRanks - 1));
+        int at = lane < R ? static_cast<int>(ld_peer32(&sh.seg_n[turn], lane)) : 0;
+        const int mine = __shfl_sync(0xffffffffu, at, warp & (R - 1));
 #pragma unroll
-        for (int o = 1; o < kRanks; o <<= 1) {
+        for (int o = 1; o < R; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, at, o);
             if (lane >= o) at += y;
         }
-        list_n = __shfl_sync(0xffffffffu, at, kRanks - 1);
-        at = __shfl_sync(0xffffffffu, at, warp & (kRanks - 1)) - mine;
-        if (warp < kRanks)
+        list_n = __shfl_sync(0xffffffffu, at, R - 1);
+        at = __shfl_sync(0xffffffffu, at, warp & (R - 1)) - mine;
+        if (warp < R)
             for (int i = lane; i < mine; i += 32) {
                 const u64 key = ld_peer64(&sh.seg_key[turn][i], warp), m = ld_peer64(&sh.seg_mass[turn][i], warp);
                 sh.key[at + i] = key;
@@ -442,7 +421,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         __syncthreads();
     };
     // Index in the list of the first token whose inclusive mass exceeds `target`.
-    auto hit_of = [&](u64 target) {
+    auto hit_of = [&](u64 target) __attribute__((always_inline)) {
         for (int i = threadIdx.x; i < list_n; i += kThreads)
             if (sh.s_pre[i] <= target && target < sh.s_pre[i + 1]) sh.hit = i;
         __syncthreads();
@@ -467,7 +446,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
             for (int y = 0; y < 4; ++y)
                 if (at[y] >= 0) atomicAdd(&sh.h[0][at[y]], 1u);
         });
-        hist_reduce<false>(sh, sh.p0, rank);
+        hist_reduce<R, false>(sh, sh.p0, rank);
         const unsigned int all = sh.p0.cnt[kBins];
         const int bin = choose_bin(sh, sh.p0, true, min(static_cast<unsigned int>(k), all) - 1);
         if (sh.p0.cnt[bin + 1] <= kCap) {
@@ -493,8 +472,22 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     }
 
     // ---- histogram of masses; the row's mass and min-p's
-    u64 zm;
-    fill(sc, mp46, [&](float l, int) { return row_bin(sc, l); }, &zm);
+    u64 zm = 0;
+    each4([&](const float (&l)[4], int) {
+        if (!within(sc, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])))) return;
+        u64 m[4];
+        int at[4];
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+            bool keep;
+            m[y] = row_mass(sh, sc, l[y], mp46, &keep);
+            zm += keep ? m[y] : 0ull;
+            at[y] = row_bin(sc, l[y]);
+        }
+#pragma unroll
+        for (int y = 0; y < 4; ++y)
+            if (m[y] != 0) hist_add(sh, at[y], m[y]);
+    });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) zm += __shfl_xor_sync(0xffffffffu, zm, o);
     if (lane == 0) sh.red_b[warp] = zm;
@@ -503,18 +496,18 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         for (int w = 1; w < kWarps; ++w) zm += sh.red_b[w];
         sh.x_zm = zm;
     }
-    hist_reduce<true>(sh, sh.p0, rank);
+    hist_reduce<R, true>(sh, sh.p0, rank);
     {
-        u64 m = lane < kRanks ? ld_peer64(&sh.x_zm, lane) : 0ull;
+        u64 m = lane < R ? ld_peer64(&sh.x_zm, lane) : 0ull;
 #pragma unroll
-        for (int o = 4; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
+        for (int o = R / 2; o > 0; o >>= 1) m += __shfl_xor_sync(0xffffffffu, m, o);
         zm = __shfl_sync(0xffffffffu, m, 0);
     }
     int have_lo = 1, have_hi = 0;              // bins that the list holds whole
     unsigned int list_cnt = 0;                 // tokens before the list
     // Index in the list of the first token whose inclusive mass (by_count: count)
     // exceeds `target`; there is one.
-    auto find = [&](bool by_count, u64 target) {
+    auto find = [&](bool by_count, u64 target) __attribute__((always_inline)) {
         const int bin = choose_bin(sh, sh.p0, by_count, target);
         if (bin < have_lo || bin > have_hi) {
             const unsigned int upto = sh.p0.cnt[bin + 1], inside0 = upto - sh.p0.cnt[bin];
@@ -530,9 +523,14 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
                 __syncthreads();
                 hist_clear(sh);
                 __syncthreads();
-                u64 unused;
-                fill(sc, mp46, [&](float l, int) { return row_bin(sc, l) == bin ? row_step(sc, l) : -1; }, &unused);
-                hist_reduce<true>(sh, sh.p1, rank);
+                auto add = [&](int at, float l) {
+                    bool keep;
+                    const u64 m = row_mass(sh, sc, l, mp46, &keep);
+                    if (m != 0) hist_add(sh, at, m);
+                };
+                each_of([&](float l, int) { return within(sc, l) && row_bin(sc, l) == bin; },
+                        [&](float l, int) { add(row_step(sc, l), l); });
+                hist_reduce<R, true>(sh, sh.p1, rank);
                 u64 before = sh.p0.mass[bin];
                 list_cnt = sh.p0.cnt[bin];
                 const int step = choose_bin(sh, sh.p1, by_count, target - (by_count ? list_cnt : before));
@@ -566,19 +564,17 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
                     sh.x_k0 = k0;
                 }
                 cluster_sync();
-                k1 = warp_max_u64(lane < kRanks ? ld_peer64(&sh.x_k1, lane) : 0ull);
-                k0 = ~warp_max_u64(lane < kRanks ? ~ld_peer64(&sh.x_k0, lane) : 0ull);
+                k1 = warp_max_u64(lane < R ? ld_peer64(&sh.x_k1, lane) : 0ull);
+                k0 = ~warp_max_u64(lane < R ? ~ld_peer64(&sh.x_k0, lane) : 0ull);
                 while (inside > kCap) {
                     const int bits = 64 - __clzll(static_cast<long long>(k1 - k0));
                     const int shift = bits > 10 ? bits - 10 : 0;
                     __syncthreads();
                     hist_clear(sh);
                     __syncthreads();
-                    fill(sc, mp46, [&](float l, int id) {
-                        const u64 key = row_key(l, id);
-                        return key >= k0 && key <= k1 ? static_cast<int>((k1 - key) >> shift) : -1;
-                    }, &unused);
-                    hist_reduce<true>(sh, sh.p1, rank);
+                    each_of([&](float l, int id) { const u64 key = row_key(l, id); return key >= k0 && key <= k1; },
+                            [&](float l, int id) { add(static_cast<int>((k1 - row_key(l, id)) >> shift), l); });
+                    hist_reduce<R, true>(sh, sh.p1, rank);
                     const int cut = choose_bin(sh, sh.p1, by_count, target - (by_count ? list_cnt : before));
                     before += sh.p1.mass[cut];
                     list_cnt += sh.p1.cnt[cut];
@@ -608,25 +604,49 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     finish(find(false, static_cast<u64>(u * static_cast<double>(z))));
 }
 
-template <bool KEPT>
+template <int R, bool KEPT>
 static int rows_go(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
                    const float* top_p, const float* min_p, const float* uniforms, int32_t* out, cudaStream_t st) {
-    constexpr int smem = static_cast<int>(sizeof(RowShared)) + (KEPT ? (kKept + 4) * 4 : 0);
+    constexpr int most = static_cast<int>(sizeof(RowShared)) + (KEPT ? (kKept + 4) * 4 : 0);
     static bool attr = false;
     if (!attr) {
-        cudaError_t e = cudaFuncSetAttribute(sample_rows_kernel<KEPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        cudaError_t e = cudaFuncSetAttribute(sample_rows_kernel<R, KEPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
         if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(sample_rows_kernel)");
         attr = true;
     }
-    sample_rows_kernel<KEPT><<<B * kRanks, kThreads, smem, st>>>(logits, V, temperature, top_k, top_p, min_p, uniforms, out);
-    LLB_CHECK_LAUNCH("sample_rows_kernel");
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(B * R);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = sizeof(RowShared) + (KEPT ? ((V + R - 1) / R + 4) * sizeof(float) : 0);
+    cfg.dynamicSmemBytes = (cfg.dynamicSmemBytes + 15) & ~size_t(15);
+    cfg.stream = st;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = R;
+    at[0].val.clusterDim.y = 1;
+    at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, sample_rows_kernel<R, KEPT>, logits, V, temperature, top_k, top_p, min_p,
+                                       uniforms, out);
+    count_launch();
+    if (e != cudaSuccess) return cuda_fail(e, "sample_rows_kernel");
     return LLAMA_OK;
+}
+
+template <int R>
+static int rows_keep(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
+                     const float* top_p, const float* min_p, const float* uniforms, int32_t* out, cudaStream_t st) {
+    if (V <= R * kKept) return rows_go<R, true>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
+    return rows_go<R, false>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
 }
 
 int launch_sample_rows(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
                        const float* top_p, const float* min_p, const float* uniforms, int32_t* out, cudaStream_t st) {
-    if (V <= kRanks * kKept) return rows_go<true>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
-    return rows_go<false>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
+    // the widest clusters whose rows all fit on the GPU at once (two CTAs an SM)
+    if (B <= 32) return rows_keep<8>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
+    if (B <= 64) return rows_keep<4>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
+    return rows_keep<2>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
 }
 
 }  // namespace llb
