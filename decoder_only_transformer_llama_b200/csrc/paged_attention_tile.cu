@@ -36,7 +36,10 @@
 namespace llb {
 
 namespace {
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;                // three warpgroups; warps 10 and 11 only fill the third
+// registers a thread: the launch's 168, of which the third warpgroup gives up
+// what the two softmax warpgroups take (2 * 216 + 72 = 3 * 168)
+constexpr int kRegsSoftmax = 216, kRegsOther = 72;
 constexpr int kRows = 256;
 constexpr int kKeys = 128;
 constexpr int kBox = 128 * 128;             // 128 rows of 64 16-bit values
@@ -54,19 +57,78 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ uint64_t pk2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void un2(uint64_t v, float& a, float& b) { asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+// 32 lanes x 16 fp32 columns from registers.
+__device__ __forceinline__ void tmem_st_16(uint32_t taddr, const float (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+        :: "r"(taddr), "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]), "f"(v[8]),
+           "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+        : "memory");
+}
+// 32 lanes x 32 columns of packed 16-bit pairs from registers.
+__device__ __forceinline__ void tmem_st_p(uint32_t taddr, const uint32_t (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+           "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15]), "r"(v[16]), "r"(v[17]),
+           "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]), "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]),
+           "r"(v[27]), "r"(v[28]), "r"(v[29]), "r"(v[30]), "r"(v[31])
+        : "memory");
+}
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         :: "r"(smem_u32(dst)), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
         : "memory");
 }
-// D[tmem] (+)= A[tmem] * B[smem desc]: A's 16-bit values two to a column, K-major.
-__device__ __forceinline__ void tc_mma_16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+// MMAs and commits by one lane of a converged warp (the same lane each time):
+// control flow and operands stay uniform over the warp, which keeps the
+// descriptors in uniform registers.
+__device__ __forceinline__ void warp_mma_ss(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+        :: "r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(acc) : "memory");
+}
+// A from TMEM: 16-bit values two to a column, K-major.
+__device__ __forceinline__ void warp_mma_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
         :: "r"(d), "r"(a), "l"(bdesc), "r"(idesc), "r"(acc) : "memory");
+}
+__device__ __forceinline__ void warp_commit(uint64_t* bar) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "elect.sync _|q, 0xffffffff;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+        :: "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
 }
 template <typename T> __device__ __forceinline__ bool not_finite16(uint32_t h) {
     constexpr uint32_t e = std::is_same<T, bf16>::value ? 0x7f80u : 0x7c00u;
@@ -93,7 +155,7 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
     long long* cum = reinterpret_cast<long long*>(ring + nslots * TILE);
     WorkReq* req = reinterpret_cast<WorkReq*>(cum + a.B + 1);
     __shared__ uint64_t kv_full[kMaxSlots], kv_empty[kMaxSlots];
-    __shared__ uint64_t q_full, q_empty, s_full[2], p_full[2], o_full[2], mdone;
+    __shared__ uint64_t q_full, q_empty, s_full[2], p_full[2][2], o_full[2], mdone;
     __shared__ long long s_scan[2 * kThreads / 32], s_tiles;
     __shared__ uint32_t tmem_slot;
     __shared__ int s_fail, s_bad, s_last[2];
@@ -114,7 +176,7 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
         for (int i = 0; i < nslots; ++i) { mbar_init(&kv_full[i], 1); mbar_init(&kv_empty[i], 1); }
         mbar_init(&q_full, 1);
         mbar_init(&q_empty, 1);
-        for (int t = 0; t < 2; ++t) { mbar_init(&s_full[t], 1); mbar_init(&p_full[t], 128); mbar_init(&o_full[t], 1); }
+        for (int t = 0; t < 2; ++t) { mbar_init(&s_full[t], 1); mbar_init(&p_full[t][0], 128); mbar_init(&p_full[t][1], 128); mbar_init(&o_full[t], 1); }
         mbar_init(&mdone, 1);
         s_fail = 0;
         s_bad = 0;
@@ -145,8 +207,11 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
     };
     auto two_halves = [&](const Segment& s) { return req[s.c.b].n - (s.c.tile << shape.lr) > half; };
 
+
     int issued = 0;                                // producer: ring slots filled
     int n_q = 0;                                   // and Q tiles asked for
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kRegsOther));
     if (warp == 9) {
         // ---------------- TMA producer: lane p brings page p of a unit
         Segment sg = first_segment();
@@ -204,7 +269,7 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
             ++nseg;
         } while (ok && next_segment(sg, left));
         if (!ok && lane == 0) atomicExch(&s_fail, 1);
-    } else if (warp == 8 && lane == 0) {
+    } else if (warp == 8) {
         // ---------------- MMA issuer
         constexpr uint32_t idesc_s = idesc_16_f32<T>(128, kKeys);
         constexpr uint32_t idesc_o = idesc_16_f32_bmn<T>(128, HD);
@@ -213,28 +278,32 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
         int slot = 0, nseg = 0;
         uint32_t full_phase = 0, p_phase[2] = {0, 0};
         bool ok = true;
-        const uint32_t q0 = smem_u32(sQ), r0 = smem_u32(ring);
+        // Operand descriptors: constant bits once, then one addition per MMA (the
+        // address field counts 16 bytes; a single thread issues, so every
+        // instruction between two MMAs adds to their spacing).
+        const uint64_t q_desc = smem_desc_k_sw128(smem_u32(sQ)), k_desc = smem_desc_k_sw128(smem_u32(ring)),
+                       v_desc = smem_desc_mn_sw128(smem_u32(ring), kBox);
         auto advance = [&]() { if (++slot == nslots) { slot = 0; full_phase ^= 1; } };
         auto scores = [&](int t, int kslot) {
-            const uint32_t qb = q0 + t * TILE, kb = r0 + kslot * TILE;
+            const uint64_t qd = q_desc + t * (TILE >> 4), kd = k_desc + static_cast<uint32_t>(kslot * (TILE >> 4));
 #pragma unroll
             for (int kk = 0; kk < HD / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * kBox + (kk & 3) * 32;
-                tc_mma_16(tmem + kColS + 128 * t, smem_desc_k_sw128(qb + off), smem_desc_k_sw128(kb + off), idesc_s, kk > 0);
+                const uint32_t off = ((kk >> 2) * kBox + (kk & 3) * 32) >> 4;
+                warp_mma_ss(tmem + kColS + 128 * t, qd + off, kd + off, idesc_s, kk > 0);
             }
-            tc_commit(&s_full[t]);
+            warp_commit(&s_full[t]);
         };
         do {
             const int nt = two_halves(sg) ? 2 : 1;
-            ok = mbar_wait(&q_full, nseg & 1) && mbar_wait(&kv_full[slot], full_phase);
+            ok = warp_wait(&q_full, nseg & 1) && warp_wait(&kv_full[slot], full_phase);
             if (!ok) break;
             tc_fence_after();
             for (int t = 0; t < nt; ++t) scores(t, slot);
-            tc_commit(&kv_empty[slot]);
-            if (sg.len == 1) tc_commit(&q_empty);
+            warp_commit(&kv_empty[slot]);
+            if (sg.len == 1) warp_commit(&q_empty);
             advance();
             for (int i = 0; ok && i < sg.len; ++i) {
-                ok = mbar_wait(&kv_full[slot], full_phase);          // V of this unit
+                ok = warp_wait(&kv_full[slot], full_phase);          // V of this unit
                 if (!ok) break;
                 const int vslot = slot;
                 advance();
@@ -243,36 +312,42 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     if (t >= nt || !ok) break;
-                    ok = mbar_wait(&p_full[t], p_phase[t]);
+                    const uint64_t vd = v_desc + static_cast<uint32_t>(vslot * (TILE >> 4));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {                    // 64 keys at a time
+                        ok = warp_wait(&p_full[t][h], p_phase[t]);
+                        if (!ok) break;
+                        tc_fence_after();
+#pragma unroll
+                        for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+                            warp_mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk,
+                                         vd + (kk * 16 * 128 >> 4), idesc_o, i > 0 || kk > 0);
+                    }
                     if (!ok) break;
                     p_phase[t] ^= 1;
-                    tc_fence_after();
-                    const uint32_t vb = r0 + vslot * TILE;
-#pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        tc_mma_16_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk,
-                                     smem_desc_mn_sw128(vb + kk * 16 * 128, kBox), idesc_o, i > 0 || kk > 0);
-                    tc_commit(&o_full[t]);
+                    warp_commit(&o_full[t]);
                     if (more) {
-                        if (t == 0) ok = mbar_wait(&kv_full[kslot], full_phase);
+                        if (t == 0) ok = warp_wait(&kv_full[kslot], full_phase);
                         if (!ok) break;
                         scores(t, kslot);
                     }
                 }
                 if (!ok) break;
-                tc_commit(&kv_empty[vslot]);
+                warp_commit(&kv_empty[vslot]);
                 if (more) {
-                    tc_commit(&kv_empty[kslot]);
-                    if (i + 2 == sg.len) tc_commit(&q_empty);
+                    warp_commit(&kv_empty[kslot]);
+                    if (i + 2 == sg.len) warp_commit(&q_empty);
                     advance();
                 }
             }
             ++nseg;
         } while (ok && next_segment(sg, left));
-        if (!ok) atomicExch(&s_fail, 1);
-        tc_commit(&mdone);                         // every MMA has finished before TMEM is freed
-        if (!mbar_wait(&mdone, 0)) atomicExch(&s_fail, 1);
-    } else if (warp < 8) {
+        if (!ok && lane == 0) atomicExch(&s_fail, 1);
+        warp_commit(&mdone);                         // every MMA has finished before TMEM is freed
+        if (!warp_wait(&mdone, 0) && lane == 0) atomicExch(&s_fail, 1);
+    }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kRegsSoftmax));
         // ---------------- softmax and epilogue: thread = row r of sub-tile t
         const int t = warp >> 2;
         const int r = tid & 127;
@@ -301,12 +376,13 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
             const int lim0 = min(rq.seq, rq.seq - rq.n + t0 + 1);              // and the tile's first row
             if (active) {
                 float m = -INFINITY, l = 0.f;
+                bool fail = false;
                 for (int i = 0; i < sg.len; ++i) {
                     const int key0 = (sg.c.j + i) * kKeys;
-                    bool ok = mbar_wait(&s_full[t], ph);
                     const bool masked = key0 + kKeys > lim0;
+                    bool ok = mbar_wait(&s_full[t], ph);
                     if (t == 0 && masked) ok = ok && mbar_wait(&kv_full[vslot], v_phase);
-                    if (named_any(1 + t, 128, !ok || *reinterpret_cast<volatile int*>(&s_fail) != 0)) { stop = true; break; }
+                    if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
                     tc_fence_after();
                     if (t == 0 && masked) {
                         // V values that some rows must not see: an infinity or
@@ -341,10 +417,16 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
 #pragma unroll
                         for (int x = 0; x < kKeys; ++x) s[x] = x < lc ? s[x] : -INFINITY;
                     }
-                    float mx = s[0];
+                    float mx;
+                    {
+                        float c[4] = {s[0], s[1], s[2], s[3]};       // four chains
 #pragma unroll
-                    for (int x = 1; x < kKeys; ++x) mx = fmaxf(mx, s[x]);
-                    mx *= sl2;
+                        for (int x = 4; x < kKeys; x += 8)
+#pragma unroll
+                            for (int y = 0; y < 4; ++y)
+                                c[y] = x + 4 + y < kKeys ? fmaxf(c[y], fmaxf(s[x + y], s[x + 4 + y])) : fmaxf(c[y], s[x + y]);
+                        mx = fmaxf(fmaxf(c[0], c[1]), fmaxf(c[2], c[3])) * sl2;
+                    }
                     bool rescale = false;
                     float corr = 1.f;
                     if (mx > m + 8.f || m == -INFINITY) {
@@ -352,53 +434,51 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
                         corr = m == -INFINITY ? 0.f : ex2(m - mx);
                         m = mx;
                     }
-                    const float ms = m == -INFINITY ? 0.f : m;       // no key so far: every weight is 0
-                    float sum0 = 0.f, sum1 = 0.f;
-                    uint32_t p[kKeys / 2];
-#pragma unroll
-                    for (int x = 0; x < kKeys; x += 2) {
-                        const float e0 = ex2(fmaf(s[x], sl2, -ms)), e1 = ex2(fmaf(s[x + 1], sl2, -ms));
-                        sum0 += e0;
-                        sum1 += e1;
-                        p[x / 2] = pack2<T>(e0, e1);
-                    }
-                    l = l * corr + (sum0 + sum1);
-#pragma unroll
-                    for (int x = 0; x < kKeys / 2; x += 32) {
-                        float f[32];
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) f[e] = __uint_as_float(p[x + e]);
-                        tmem_st_32x32b_x32(colS + x, f);
-                    }
                     if (__any_sync(0xffffffffu, rescale)) {
-                        // the previous product has to have finished with O
-                        ok = __all_sync(0xffffffffu, mbar_wait(&o_full[t], ph ^ 1));
-                        tc_fence_after();
-                        if (ok) {
+                        // O holds every earlier unit: these scores came behind its last product
 #pragma unroll 1
-                            for (int x = 0; x < HD; x += 32) {
-                                float o[32];
-                                tmem_ld_32x32b_x32(colO + x, o);
-                                tc_wait_ld();
+                        for (int x = 0; x < HD; x += 16) {
+                            float o[16];
+                            tmem_ld_32x32b_x16(colO + x, o);
+                            tc_wait_ld();
 #pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] *= corr;
-                                tmem_st_32x32b_x32(colO + x, o);
-                            }
-                        } else if (lane == 0) {
-                            atomicExch(&s_fail, 1);                  // seen by all at the next unit or the end
+                            for (int e = 0; e < 16; ++e) o[e] *= corr;
+                            tmem_st_16(colO + x, o);
                         }
                     }
-                    tc_wait_st();
-                    tc_fence_before();
-                    mbar_arrive(&p_full[t]);
+                    const float ms = m == -INFINITY ? 0.f : m;       // no key so far: every weight is 0
+                    const uint64_t scale2 = pk2(sl2, sl2), minus2 = pk2(-ms, -ms);
+                    uint64_t sum2[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t p[32];
+#pragma unroll
+                        for (int x = 0; x < 32; ++x) {
+                            float e0, e1;
+                            un2(fma2(pk2(s[64 * h + 2 * x], s[64 * h + 2 * x + 1]), scale2, minus2), e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            sum2[x & 1] = add2(sum2[x & 1], pk2(e0, e1));
+                            p[x] = pack2<T>(e0, e1);
+                        }
+                        tmem_st_p(colS + 32 * h, p);
+                        tc_wait_st();
+                        tc_fence_before();
+                        mbar_arrive(&p_full[t][h]);
+                    }
+                    {
+                        float a0, a1;
+                        un2(add2(sum2[0], sum2[1]), a0, a1);
+                        l = l * corr + (a0 + a1);
+                    }
                     ph ^= 1;
                     vslot += 2;
                     if (vslot >= nslots) { vslot -= nslots; v_phase ^= 1; }
                 }
-                if (stop) break;
                 // ---- end of the tile, or of this CTA's part of it: O holds every unit
-                const bool ok = mbar_wait(&o_full[t], ph ^ 1);
-                if (named_any(1 + t, 128, !ok || *reinterpret_cast<volatile int*>(&s_fail) != 0)) { stop = true; break; }
+                if (!fail) fail = !mbar_wait(&o_full[t], ph ^ 1);
+                stop = named_any(1 + t, 128, fail);
+                if (stop) break;
                 tc_fence_after();
                 const bool whole = sg.c.j == 0 && sg.len == sg.c.nu;
                 const long long tile_u0 = u0 + done - sg.c.j;
