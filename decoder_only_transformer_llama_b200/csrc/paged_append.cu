@@ -7,7 +7,9 @@
 //
 // in fp32, rounded once to the cache's type.  Bound by HBM: every value is
 // read once and written once.  A lane holds 16 bytes of one head; the
-// HD * sizeof(input) / 16 lanes of a head sum its squares by shuffles.
+// HD * sizeof(input) / 16 lanes of a head sum its squares by shuffles.  A thread
+// asks for its kHeads heads' values, the rotation and the slot together, so that
+// a CTA waits for memory once and then once more for what the position selects.
 #include <type_traits>
 
 #include "common.cuh"
@@ -18,12 +20,19 @@ namespace llb {
 namespace {
 constexpr int kThreads = 256;
 
+constexpr int kHeads = 4;      // heads a thread works on
+
 template <typename TI, int N>
-__device__ __forceinline__ void load_vec(const TI* p, float (&v)[N]) {
-    const uint4 u = *reinterpret_cast<const uint4*>(p);
+__device__ __forceinline__ void unpack(const uint4& u, float (&v)[N]) {
     const TI* h = reinterpret_cast<const TI*>(&u);
 #pragma unroll
     for (int i = 0; i < N; ++i) v[i] = to_f32<TI>(h[i]);
+}
+// 16 bytes that are read once.
+__device__ __forceinline__ uint4 load_once(const void* p) {
+    uint4 u;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "l"(p));
+    return u;
 }
 
 template <typename TO, int N>
@@ -50,53 +59,66 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
     constexpr int LPH = HD / N;                            // lanes per head
     constexpr int GROUPS = kThreads / LPH;
     const int t = blockIdx.x;
+    const int sub = threadIdx.x % LPH;
+    const int heads = a.nh + 2 * a.nkv;
+    const int h0 = blockIdx.y * (GROUPS * kHeads) + threadIdx.x / LPH;
     const long long slot = a.slots[t];
-    if (slot < 0) return;                                  // padding: nothing is written
     const int pos = a.positions[t];
+    uint4 raw[kHeads];
+#pragma unroll
+    for (int e = 0; e < kHeads; ++e) {
+        const int h = h0 + e * GROUPS;
+        raw[e] = make_uint4(0u, 0u, 0u, 0u);
+        if (h >= heads) continue;
+        const TI* src = h < a.nh ? static_cast<const TI*>(a.q) + t * a.q_stride + h * HD
+                      : h < a.nh + a.nkv ? static_cast<const TI*>(a.k) + t * a.k_stride + (h - a.nh) * HD
+                                         : static_cast<const TI*>(a.v) + t * a.v_stride + (h - a.nh - a.nkv) * HD;
+        raw[e] = load_once(src + sub * N);
+    }
+    if (slot < 0) return;                                  // padding: nothing is written
     if (slot >= a.n_slots || pos < 0 || pos >= a.rope_len) {
         if (threadIdx.x == 0) report_status(a.status, LLAMA_ERR_CAPACITY);
         return;
     }
-    const int sub = threadIdx.x % LPH;
+    float cs[N / 2], sn[N / 2];
+    {
+        const float4* r = reinterpret_cast<const float4*>(a.rope + static_cast<long long>(pos) * (HD / 2) + sub * (N / 2));
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) {
+            const float4 f = __ldg(r + i);
+            cs[2 * i] = f.x; sn[2 * i] = f.y; cs[2 * i + 1] = f.z; sn[2 * i + 1] = f.w;
+        }
+    }
     const long long page = slot >> a.page_shift;
     const long long off = slot & ((1LL << a.page_shift) - 1);
-    float cs[N], sn[N];
-    {
-        const float2* r = a.rope + static_cast<long long>(pos) * (HD / 2) + sub * (N / 2);
+    const bool norms = a.q_norm || a.k_norm;
 #pragma unroll
-        for (int i = 0; i < N / 2; ++i) { const float2 f = r[i]; cs[i] = f.x; sn[i] = f.y; }
-    }
-    const int heads = a.nh + 2 * a.nkv;
-    for (int h0 = blockIdx.y * GROUPS; h0 < heads; h0 += gridDim.y * GROUPS) {
-        const int h = h0 + threadIdx.x / LPH;
-        const bool live = h < heads;
-        const bool is_q = h < a.nh, is_k = !is_q && h < a.nh + a.nkv;
-        const TI* src = is_q ? static_cast<const TI*>(a.q) + t * a.q_stride + h * HD
-                      : is_k ? static_cast<const TI*>(a.k) + t * a.k_stride + (h - a.nh) * HD
-                             : static_cast<const TI*>(a.v) + t * a.v_stride + (h - a.nh - a.nkv) * HD;
+    for (int e = 0; e < kHeads; ++e) {
+        const int h = h0 + e * GROUPS;
+        const bool live = h < heads, is_q = h < a.nh, is_k = !is_q && h < a.nh + a.nkv;
         float x[N];
-        if (live) load_vec<TI, N>(src + sub * N, x);
-        else {
-#pragma unroll
-            for (int i = 0; i < N; ++i) x[i] = 0.f;
-        }
-        const float* w = is_q ? a.q_norm : is_k ? a.k_norm : nullptr;
-        if (a.q_norm || a.k_norm) {                        // the same for every thread: shuffles stay warp-wide
+        unpack<TI, N>(raw[e], x);
+        if (norms) {                                       // the same for every thread: the shuffles stay warp-wide
             float ss = 0.f;
 #pragma unroll
             for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
 #pragma unroll
             for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            const float* w = is_q ? a.q_norm : is_k ? a.k_norm : nullptr;
             if (w) {
                 const float inv = 1.f / sqrtf(ss / HD + a.eps);
 #pragma unroll
-                for (int i = 0; i < N; ++i) x[i] = x[i] * inv * w[sub * N + i];
+                for (int i = 0; i < N; i += 4) {
+                    const float4 f = __ldg(reinterpret_cast<const float4*>(w + sub * N + i));
+                    x[i] *= inv * f.x; x[i + 1] *= inv * f.y; x[i + 2] *= inv * f.z; x[i + 3] *= inv * f.w;
+                }
             }
         }
         if (!live) continue;
         TO* dst;
-        if (is_q) dst = static_cast<TO*>(a.q_out) + (static_cast<long long>(t) * a.nh + h) * HD;
-        else {
+        if (is_q) {
+            dst = static_cast<TO*>(a.q_out) + (static_cast<long long>(t) * a.nh + h) * HD;
+        } else {
             const int g = is_k ? h - a.nh : h - a.nh - a.nkv;
             dst = static_cast<TO*>(is_k ? a.k_pages : a.v_pages) +
                   (((page * a.nkv + g) << a.page_shift) + off) * HD;
@@ -109,6 +131,8 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
                 y[2 * i + 1] = x[2 * i] * sn[i] + x[2 * i + 1] * cs[i];
             }
             store_vec<TO, N>(dst + sub * N, y);
+        } else if constexpr (std::is_same<TI, TO>::value) {
+            *reinterpret_cast<uint4*>(dst + sub * N) = raw[e];     // the value's own bits
         } else {
             store_vec<TO, N>(dst + sub * N, x);
         }
@@ -117,7 +141,9 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
 
 template <typename TI, typename TO, int HD>
 static int append_go(const AppendArgs& a, cudaStream_t st) {
-    paged_append_kernel<TI, TO, HD><<<dim3(a.T, 1), kThreads, 0, st>>>(a);
+    constexpr int per = kThreads / (HD * static_cast<int>(sizeof(TI)) / 16) * kHeads;   // heads a CTA works on
+    const int heads = a.nh + 2 * a.nkv;
+    paged_append_kernel<TI, TO, HD><<<dim3(a.T, (heads + per - 1) / per), kThreads, 0, st>>>(a);
     LLB_CHECK_LAUNCH("paged_append_kernel");
     return LLAMA_OK;
 }

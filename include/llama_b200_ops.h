@@ -128,7 +128,7 @@ LLAMA_API int llama_rope_table(float* rope, int len, int head_dim, float theta, 
  *   q_out       [T, n_heads, head_dim] in the cache's dtype (may be q itself if
  *               that has this type and layout); K and V go to k_pages, v_pages
  * fp32 arithmetic, one rounding; v of the cache's dtype is copied.  A row with
- * slot < 0 is padding: nothing of it is read or written.  A row with a slot
+ * slot < 0 is padding: nothing of it is written.  A row with a slot
  * outside the pool or a position outside the table writes nothing and sets
  * LLAMA_ERR_CAPACITY in status.  The slots of one call must differ.  Bases,
  * rows, rope and norm weights 16-byte aligned. */
