@@ -6,10 +6,17 @@
 //   (y[2j], y[2j+1]) -> (y[2j] c - y[2j+1] s, y[2j] s + y[2j+1] c),  (c, s) = rope[position][j]
 //
 // in fp32, rounded once to the cache's type.  Bound by HBM: every value is
-// read once and written once.  A lane holds 16 bytes of one head; the
-// HD * sizeof(input) / 16 lanes of a head sum its squares by shuffles.  A thread
-// asks for its kHeads heads' values, the rotation and the slot together, so that
-// a CTA waits for memory once and then once more for what the position selects.
+// read once and written once.  A lane holds two vectors of 16 bytes of a head,
+// half a head apart (each coalesced, and the work per head shared by twice the
+// values); the HD * sizeof(input) / 32 lanes of a head sum its squares by
+// shuffles.  A thread asks for its kHeads heads' values and the slot together,
+// so that a CTA waits for memory once and then once more for the rotation, which
+// serves all of its heads.  What a thread does besides its heads costs about as
+// much as one of them: three heads a thread where a token has enough, one where
+// a CTA takes a token in one go or the step is short (16384 tokens of 48 heads,
+// 16-bit, with norms: 85 us with three, 122 with one and 105 with two in CTAs of
+// 256, which leave a quarter of the places empty; 64 tokens of 80 heads: 2.5 us
+// with one, 2.9 with three).
 #include <type_traits>
 
 #include "common.cuh"
@@ -18,9 +25,7 @@
 namespace llb {
 
 namespace {
-constexpr int kThreads = 256;
-
-constexpr int kHeads = 4;      // heads a thread works on
+constexpr int kThreads = 128;
 
 template <typename TI, int N>
 __device__ __forceinline__ void unpack(const uint4& u, float (&v)[N]) {
@@ -53,10 +58,10 @@ __device__ __forceinline__ void store_vec(TO* p, const float (&v)[N]) {
 }
 }  // namespace
 
-template <typename TI, typename TO, int HD>
+template <typename TI, typename TO, int HD, int kHeads>
 __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
-    constexpr int N = 16 / static_cast<int>(sizeof(TI));   // values per lane
-    constexpr int LPH = HD / N;                            // lanes per head
+    constexpr int N = 16 / static_cast<int>(sizeof(TI));   // values per vector
+    constexpr int LPH = HD / (2 * N);                      // lanes per head
     constexpr int GROUPS = kThreads / LPH;
     const int t = blockIdx.x;
     const int sub = threadIdx.x % LPH;
@@ -64,54 +69,62 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
     const int h0 = blockIdx.y * (GROUPS * kHeads) + threadIdx.x / LPH;
     const long long slot = a.slots[t];
     const int pos = a.positions[t];
-    uint4 raw[kHeads];
+    const TI* rows[3] = {static_cast<const TI*>(a.q) + t * a.q_stride,
+                         static_cast<const TI*>(a.k) + t * a.k_stride - a.nh * HD,
+                         static_cast<const TI*>(a.v) + t * a.v_stride - (a.nh + a.nkv) * HD};
+    uint4 raw[kHeads][2];
 #pragma unroll
     for (int e = 0; e < kHeads; ++e) {
         const int h = h0 + e * GROUPS;
-        raw[e] = make_uint4(0u, 0u, 0u, 0u);
+        raw[e][0] = raw[e][1] = make_uint4(0u, 0u, 0u, 0u);
         if (h >= heads) continue;
-        const TI* src = h < a.nh ? static_cast<const TI*>(a.q) + t * a.q_stride + h * HD
-                      : h < a.nh + a.nkv ? static_cast<const TI*>(a.k) + t * a.k_stride + (h - a.nh) * HD
-                                         : static_cast<const TI*>(a.v) + t * a.v_stride + (h - a.nh - a.nkv) * HD;
-        raw[e] = load_once(src + sub * N);
+        const TI* src = (h < a.nh ? rows[0] : h < a.nh + a.nkv ? rows[1] : rows[2]) + h * HD + sub * N;
+        raw[e][0] = load_once(src);
+        raw[e][1] = load_once(src + HD / 2);
     }
     if (slot < 0) return;                                  // padding: nothing is written
     if (slot >= a.n_slots || pos < 0 || pos >= a.rope_len) {
         if (threadIdx.x == 0) report_status(a.status, LLAMA_ERR_CAPACITY);
         return;
     }
-    float cs[N / 2], sn[N / 2];
-    {
-        const float4* r = reinterpret_cast<const float4*>(a.rope + static_cast<long long>(pos) * (HD / 2) + sub * (N / 2));
+    float cs[N], sn[N];                                    // of both vectors' pairs
+#pragma unroll
+    for (int v = 0; v < 2; ++v) {
+        const float4* r = reinterpret_cast<const float4*>(a.rope + static_cast<long long>(pos) * (HD / 2) + v * (HD / 4) + sub * (N / 2));
 #pragma unroll
         for (int i = 0; i < N / 4; ++i) {
             const float4 f = __ldg(r + i);
-            cs[2 * i] = f.x; sn[2 * i] = f.y; cs[2 * i + 1] = f.z; sn[2 * i + 1] = f.w;
+            cs[v * (N / 2) + 2 * i] = f.x; sn[v * (N / 2) + 2 * i] = f.y;
+            cs[v * (N / 2) + 2 * i + 1] = f.z; sn[v * (N / 2) + 2 * i + 1] = f.w;
         }
     }
-    const long long page = slot >> a.page_shift;
-    const long long off = slot & ((1LL << a.page_shift) - 1);
+    // a position's rows of one page's heads lie 2^page_shift rows apart
+    const long long cell = (((slot >> a.page_shift) * a.nkv) << a.page_shift) + (slot & ((1LL << a.page_shift) - 1));
     const bool norms = a.q_norm || a.k_norm;
 #pragma unroll
     for (int e = 0; e < kHeads; ++e) {
         const int h = h0 + e * GROUPS;
         const bool live = h < heads, is_q = h < a.nh, is_k = !is_q && h < a.nh + a.nkv;
-        float x[N];
-        unpack<TI, N>(raw[e], x);
+        float x[2][N];
+        unpack<TI, N>(raw[e][0], x[0]);
+        unpack<TI, N>(raw[e][1], x[1]);
         if (norms) {                                       // the same for every thread: the shuffles stay warp-wide
-            float ss = 0.f;
+            float s0 = 0.f, s1 = 0.f;
 #pragma unroll
-            for (int i = 0; i < N; ++i) ss = fmaf(x[i], x[i], ss);
+            for (int i = 0; i < N; ++i) { s0 = fmaf(x[0][i], x[0][i], s0); s1 = fmaf(x[1][i], x[1][i], s1); }
+            s0 += s1;
 #pragma unroll
-            for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            for (int o = LPH / 2; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
             const float* w = is_q ? a.q_norm : is_k ? a.k_norm : nullptr;
             if (w) {
-                const float inv = 1.f / sqrtf(ss / HD + a.eps);
+                const float inv = rsqrtf(s0 * (1.f / HD) + a.eps);
 #pragma unroll
-                for (int i = 0; i < N; i += 4) {
-                    const float4 f = __ldg(reinterpret_cast<const float4*>(w + sub * N + i));
-                    x[i] *= inv * f.x; x[i + 1] *= inv * f.y; x[i + 2] *= inv * f.z; x[i + 3] *= inv * f.w;
-                }
+                for (int v = 0; v < 2; ++v)
+#pragma unroll
+                    for (int i = 0; i < N; i += 4) {
+                        const float4 f = __ldg(reinterpret_cast<const float4*>(w + v * (HD / 2) + sub * N + i));
+                        x[v][i] *= inv * f.x; x[v][i + 1] *= inv * f.y; x[v][i + 2] *= inv * f.z; x[v][i + 3] *= inv * f.w;
+                    }
             }
         }
         if (!live) continue;
@@ -120,30 +133,38 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
             dst = static_cast<TO*>(a.q_out) + (static_cast<long long>(t) * a.nh + h) * HD;
         } else {
             const int g = is_k ? h - a.nh : h - a.nh - a.nkv;
-            dst = static_cast<TO*>(is_k ? a.k_pages : a.v_pages) +
-                  (((page * a.nkv + g) << a.page_shift) + off) * HD;
+            dst = static_cast<TO*>(is_k ? a.k_pages : a.v_pages) + (cell + (static_cast<long long>(g) << a.page_shift)) * HD;
         }
-        if (is_q || is_k) {
-            float y[N];
+        dst += sub * N;
 #pragma unroll
-            for (int i = 0; i < N / 2; ++i) {
-                y[2 * i] = x[2 * i] * cs[i] - x[2 * i + 1] * sn[i];
-                y[2 * i + 1] = x[2 * i] * sn[i] + x[2 * i + 1] * cs[i];
+        for (int v = 0; v < 2; ++v) {
+            if (is_q || is_k) {
+                float y[N];
+#pragma unroll
+                for (int i = 0; i < N / 2; ++i) {
+                    const float c = cs[v * (N / 2) + i], n = sn[v * (N / 2) + i];
+                    y[2 * i] = x[v][2 * i] * c - x[v][2 * i + 1] * n;
+                    y[2 * i + 1] = x[v][2 * i] * n + x[v][2 * i + 1] * c;
+                }
+                store_vec<TO, N>(dst + v * (HD / 2), y);
+            } else if constexpr (std::is_same<TI, TO>::value) {
+                *reinterpret_cast<uint4*>(dst + v * (HD / 2)) = raw[e][v];     // the value's own bits
+            } else {
+                store_vec<TO, N>(dst + v * (HD / 2), x[v]);
             }
-            store_vec<TO, N>(dst + sub * N, y);
-        } else if constexpr (std::is_same<TI, TO>::value) {
-            *reinterpret_cast<uint4*>(dst + sub * N) = raw[e];     // the value's own bits
-        } else {
-            store_vec<TO, N>(dst + sub * N, x);
         }
     }
 }
 
 template <typename TI, typename TO, int HD>
 static int append_go(const AppendArgs& a, cudaStream_t st) {
-    constexpr int per = kThreads / (HD * static_cast<int>(sizeof(TI)) / 16) * kHeads;   // heads a CTA works on
+    constexpr int groups = kThreads / (HD * static_cast<int>(sizeof(TI)) / 32);   // heads a CTA works on at a time
     const int heads = a.nh + 2 * a.nkv;
-    paged_append_kernel<TI, TO, HD><<<dim3(a.T, (heads + per - 1) / per), kThreads, 0, st>>>(a);
+    const int one = (heads + groups - 1) / groups;
+    if (one == 1 || static_cast<long long>(a.T) * one <= 1024)
+        paged_append_kernel<TI, TO, HD, 1><<<dim3(a.T, one), kThreads, 0, st>>>(a);
+    else
+        paged_append_kernel<TI, TO, HD, 3><<<dim3(a.T, (one + 2) / 3), kThreads, 0, st>>>(a);
     LLB_CHECK_LAUNCH("paged_append_kernel");
     return LLAMA_OK;
 }
