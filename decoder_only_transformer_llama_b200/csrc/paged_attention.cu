@@ -99,6 +99,102 @@ template <typename T> __device__ __forceinline__ bool not_finite16(uint32_t h) {
 }
 }  // namespace
 
+// The partial results of a tile's contributors cf .. cl (contributor x published
+// in slot 2 x, the first one in slot 2 cf + 1), merged in their order: per step
+// of at most `step` contributors their (m, l) into shared memory, the rows'
+// maxima and weights from there, then the outputs, a thread holding four
+// columns of a row with kDeep loads in flight.  Row r of the tile lies at
+// out + (r >> lrep) * token + (r & (2^lrep - 1)) * HD and sees lim0 + (r >> lrep) keys.
+
+template <typename T, int HD>
+__device__ __forceinline__ void merge_tile(const float2* part_ml, const float* part_o, int cf, int cl, int rows,
+                                        float2* s_ml, int step, T* out, int lrep, long long token, int lim0) {
+    constexpr int kMine = kRows * (HD / 4) / kThreads;
+    constexpr int kDeep = 8;
+    __shared__ float s_top[kRows], s_sum[kRows], s_corr[kRows];
+    const int tid = threadIdx.x;
+    auto slot_of = [&](int x) { return static_cast<long long>(2 * x + (x == cf ? 1 : 0)) * kRows; };
+    if (tid < kRows) { s_top[tid] = -INFINITY; s_sum[tid] = 0.f; }
+    float4 o[kMine];
+#pragma unroll
+    for (int y = 0; y < kMine; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x0 = cf; x0 <= cl; x0 += step) {
+        const int nx = min(step, cl + 1 - x0);
+        __syncthreads();
+#pragma unroll 4
+        for (int i = tid; i < nx * kRows; i += kThreads) {
+            const int r = i % kRows;
+            if (r < rows) s_ml[i] = __ldcg(&part_ml[slot_of(x0 + i / kRows) + r]);
+        }
+        __syncthreads();
+        {
+            // eight threads a row
+            const int r = tid >> 3;
+            float M = s_top[r], L = 0.f;
+            const float before = M;
+            if (r < rows)
+                for (int x = tid & 7; x < nx; x += 8) M = fmaxf(M, s_ml[x * kRows + r].x);
+#pragma unroll
+            for (int e = 4; e > 0; e >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, e));
+            const float Ms = M == -INFINITY ? 0.f : M;
+            if (r < rows)
+                for (int x = tid & 7; x < nx; x += 8) {
+                    const float2 ml = s_ml[x * kRows + r];
+                    const float f = ex2(ml.x - Ms);
+                    L += ml.y * f;
+                    s_ml[x * kRows + r].x = f;
+                }
+#pragma unroll
+            for (int e = 4; e > 0; e >>= 1) L += __shfl_xor_sync(0xffffffffu, L, e);
+            if ((tid & 7) == 0) {
+                const float corr = ex2(before - Ms);
+                s_corr[r] = corr;
+                s_sum[r] = s_sum[r] * corr + L;
+                s_top[r] = M;
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int y = 0; y < kMine; ++y) {
+            const int idx = tid + y * kThreads, r = idx / (HD / 4), d = (idx % (HD / 4)) * 4;
+            if (r >= rows) break;
+            const float corr = s_corr[r];
+            o[y].x *= corr; o[y].y *= corr; o[y].z *= corr; o[y].w *= corr;
+#pragma unroll 1
+            for (int x = 0; x < nx; x += kDeep) {
+                float4 v[kDeep];
+#pragma unroll
+                for (int z = 0; z < kDeep; ++z)
+                    if (x + z < nx) v[z] = __ldcg(reinterpret_cast<const float4*>(part_o + (slot_of(x0 + x + z) + r) * HD + d));
+#pragma unroll
+                for (int z = 0; z < kDeep; ++z) {
+                    if (x + z >= nx) break;
+                    const float f = s_ml[(x + z) * kRows + r].x;
+                    o[y].x = fmaf(v[z].x, f, o[y].x); o[y].y = fmaf(v[z].y, f, o[y].y);
+                    o[y].z = fmaf(v[z].z, f, o[y].z); o[y].w = fmaf(v[z].w, f, o[y].w);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int y = 0; y < kMine; ++y) {
+        const int idx = tid + y * kThreads, r = idx / (HD / 4), d = (idx % (HD / 4)) * 4;
+        if (r >= rows) break;
+        const float L = s_sum[r];
+        T* dst = out + (r >> lrep) * token + (r & ((1 << lrep) - 1)) * HD + d;
+        const float4 v = lim0 + (r >> lrep) > 0 ? make_float4(o[y].x / L, o[y].y / L, o[y].z / L, o[y].w / L)
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+        if constexpr (sizeof(T) == 2) {
+            uint2 w;
+            w.x = pack2<T>(v.x, v.y);
+            w.y = pack2<T>(v.z, v.w);
+            *reinterpret_cast<uint2*>(dst) = w;
+        } else {
+            *reinterpret_cast<float4*>(dst) = v;
+        }
+    }
+}
+
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a, TileShape shape) {
     constexpr bool H16 = sizeof(T) == 2;
@@ -148,6 +244,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
         itable = a.block_tables + static_cast<long long>(ic.b) * a.max_pages;
     };
     issue_tile();
+    WorkCur cc = ic;                              // the unit at hand
     auto load_pages = [&]() {
 #pragma unroll
         for (int i = 0; i < NPG; ++i) {
@@ -207,7 +304,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
     }
 
     // ---- the tile at hand
-    WorkCur cc = work_at(shape, req, cum, a.B, a.nkv, u0);
     WorkReq rq = {0, 0, 0};
     int t0 = 0, lim0 = 0, kend = 0, rows = 0;     // first token, keys its first and last row see, rows in use
     const float sl2 = a.scale * 1.4426950408889634f;
@@ -429,9 +525,25 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
                 l2[x] += __shfl_xor_sync(0xffffffffu, l2[x], 2);
                 if (tq == 0) { s_m[warp][g8 + 8 * x] = m2[x]; s_l[warp][g8 + 8 * x] = l2[x]; }
             }
+            __syncthreads();
+            if (tid < kRows) {                    // each row's maximum, sum and the warps' weights
+                float M = -INFINITY, L = 0.f;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w][tid]);
+                const float Ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const float f = ex2(s_m[w][tid] - Ms);
+                    L += s_l[w][tid] * f;
+                    s_m[w][tid] = f;
+                }
+                s_l[0][tid] = L;
+                if (!whole && tid < rows) part_ml[slot * kRows + tid] = make_float2(M, L);
+            }
             float* s_o = reinterpret_cast<float*>(scr);          // [4 warps][4 rows][HD]
+            constexpr int CG4 = HD / 4;                          // four columns a thread
             for (int r0 = 0; r0 < rows; r0 += 4) {
-                __syncthreads();
+                if (r0) __syncthreads();
                 if ((g8 >> 2) == ((r0 >> 2) & 1)) {
                     const int x = r0 >> 3;                       // rows g8 or g8 + 8
                     float* d = s_o + (warp * 4 + (g8 & 3)) * HD + 2 * tq;
@@ -441,35 +553,38 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
                             x ? make_float2(oacc[nd][2], oacc[nd][3]) : make_float2(oacc[nd][0], oacc[nd][1]);
                 }
                 __syncthreads();
-                for (int idx = tid; idx < 4 * HD; idx += kThreads) {
-                    const int r = r0 + idx / HD, d = idx % HD;
-                    if (r >= rows) break;
-                    float M = -INFINITY, L = 0.f, acc = 0.f;
+                const int r = r0 + tid / CG4, d = (tid % CG4) * 4;
+                if (tid >= 4 * CG4 || r >= rows) continue;
+                float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-                    for (int w = 0; w < 4; ++w) M = fmaxf(M, s_m[w][r]);
-                    const float Ms = M == -INFINITY ? 0.f : M;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w) {
-                        const float f = ex2(s_m[w][r] - Ms);
-                        L += s_l[w][r] * f;
-                        acc += s_o[(w * 4 + (r & 3)) * HD + d] * f;
+                for (int w = 0; w < 4; ++w) {
+                    const float4 v = *reinterpret_cast<const float4*>(s_o + (w * 4 + (r & 3)) * HD + d);
+                    const float f = s_m[w][r];
+                    o.x = fmaf(v.x, f, o.x); o.y = fmaf(v.y, f, o.y); o.z = fmaf(v.z, f, o.z); o.w = fmaf(v.w, f, o.w);
+                }
+                const int lim = limit(r);
+                if (s_bad) {                                     // infinities and NaN taken out of V above
+                    for (int k = max(max(lim0, 0), seg_j0 * KU); k < min(lim, (cc.j + 1) * KU); ++k) {
+                        const int page = a.block_tables[static_cast<long long>(cc.b) * a.max_pages + (k >> a.page_shift)];
+                        if (page < 0 || page >= a.n_pages) continue;
+                        float v[4];
+                        load4_16<T>(vp + (((static_cast<long long>(page) * a.nkv + cc.g) << a.page_shift) +
+                                          (k & ((1 << a.page_shift) - 1))) * HD + d, v);
+                        if (!(fabsf(v[0]) < INFINITY)) o.x += v[0];
+                        if (!(fabsf(v[1]) < INFINITY)) o.y += v[1];
+                        if (!(fabsf(v[2]) < INFINITY)) o.z += v[2];
+                        if (!(fabsf(v[3]) < INFINITY)) o.w += v[3];
                     }
-                    const int lim = limit(r);
-                    if (s_bad) {                                 // infinities and NaN taken out of V above
-                        for (int k = max(lim0, seg_j0 * KU); k < min(lim, (cc.j + 1) * KU); ++k) {
-                            const int page = a.block_tables[static_cast<long long>(cc.b) * a.max_pages + (k >> a.page_shift)];
-                            if (k < 0 || page < 0 || page >= a.n_pages) continue;
-                            const float v = to_f32<T>(vp[(((static_cast<long long>(page) * a.nkv + cc.g) << a.page_shift) +
-                                                          (k & ((1 << a.page_shift) - 1))) * HD + d]);
-                            if (!(fabsf(v) < INFINITY)) acc += v;
-                        }
-                    }
-                    if (whole) {
-                        out_at(r)[d] = from_f32<T>(lim > 0 ? acc / L : 0.f);
-                    } else {
-                        part_o[(static_cast<long long>(slot) * kRows + r) * HD + d] = acc;
-                        if (d == 0) part_ml[slot * kRows + r] = make_float2(M, L);
-                    }
+                }
+                if (whole) {
+                    const float inv = lim > 0 ? 1.f / s_l[0][r] : 0.f;
+                    if (lim <= 0) o = make_float4(0.f, 0.f, 0.f, 0.f);
+                    uint2 y;
+                    y.x = pack2<T>(o.x * inv, o.y * inv);
+                    y.y = pack2<T>(o.z * inv, o.w * inv);
+                    *reinterpret_cast<uint2*>(out_at(r) + d) = y;
+                } else {
+                    *reinterpret_cast<float4*>(part_o + (static_cast<long long>(slot) * kRows + r) * HD + d) = o;
                 }
             }
         } else {
@@ -506,68 +621,9 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
             __syncthreads();
             if (s_last) {
                 __threadfence();
-                // Contributor x published in slot 2 x, the first one in slot 2 cf + 1.
-                // Per row: the maximum and the weighted sum by a warp, lane = contributor;
-                // then the outputs, a thread holding four columns of kMine rows, with
-                // the weights of kMergeStep contributors at a time in shared memory.
-                auto slot_of = [&](int x) { return static_cast<long long>(2 * x + (x == cf ? 1 : 0)) * kRows; };
-                for (int r = warp; r < rows; r += kThreads / 32) {
-                    float M = -INFINITY, L = 0.f;
-                    for (int x = cf + lane; x <= cl; x += 32) M = fmaxf(M, __ldcg(&part_ml[slot_of(x) + r].x));
-                    M = warp_max(M);
-                    const float Ms = M == -INFINITY ? 0.f : M;
-                    for (int x = cf + lane; x <= cl; x += 32) {
-                        const float2 ml = __ldcg(&part_ml[slot_of(x) + r]);
-                        L += ml.y * ex2(ml.x - Ms);
-                    }
-                    L = warp_sum(L);
-                    if (lane == 0) { s_m[0][r] = Ms; s_l[0][r] = L; }
-                }
-                constexpr int kMergeStep = 64;
-                constexpr int kMine = kRows * (HD / 4) / kThreads;
-                float* s_f = reinterpret_cast<float*>(scr);      // [kMergeStep][kRows]
-                float4 o[kMine];
-#pragma unroll
-                for (int y = 0; y < kMine; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-                for (int x0 = cf; x0 <= cl; x0 += kMergeStep) {
-                    const int nx = min(kMergeStep, cl + 1 - x0);
-                    __syncthreads();
-                    for (int idx = tid; idx < nx * kRows; idx += kThreads) {
-                        const int r = idx % kRows;
-                        if (r < rows) s_f[idx] = ex2(__ldcg(&part_ml[slot_of(x0 + idx / kRows) + r].x) - s_m[0][r]);
-                    }
-                    __syncthreads();
-#pragma unroll
-                    for (int y = 0; y < kMine; ++y) {
-                        const int idx = tid + y * kThreads, r = idx / (HD / 4), d = (idx % (HD / 4)) * 4;
-                        if (r >= rows) break;
-#pragma unroll 8
-                        for (int x = 0; x < nx; ++x) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(part_o + (slot_of(x0 + x) + r) * HD + d));
-                            const float f = s_f[x * kRows + r];
-                            o[y].x = fmaf(v.x, f, o[y].x); o[y].y = fmaf(v.y, f, o[y].y);
-                            o[y].z = fmaf(v.z, f, o[y].z); o[y].w = fmaf(v.w, f, o[y].w);
-                        }
-                    }
-                }
-#pragma unroll
-                for (int y = 0; y < kMine; ++y) {
-                    const int idx = tid + y * kThreads, r = idx / (HD / 4), d = (idx % (HD / 4)) * 4;
-                    if (r >= rows) break;
-                    const float L = s_l[0][r];
-                    const bool some = limit(r) > 0;
-                    T* dst = out_at(r) + d;
-                    const float4 v = some ? make_float4(o[y].x / L, o[y].y / L, o[y].z / L, o[y].w / L)
-                                          : make_float4(0.f, 0.f, 0.f, 0.f);
-                    if constexpr (H16) {
-                        uint2 w;
-                        w.x = pack2<T>(v.x, v.y);
-                        w.y = pack2<T>(v.z, v.w);
-                        *reinterpret_cast<uint2*>(dst) = w;
-                    } else {
-                        *reinterpret_cast<float4*>(dst) = v;
-                    }
-                }
+                merge_tile<T, HD>(part_ml, part_o, cf, cl, rows, reinterpret_cast<float2*>(scr), SCR / (kRows * 8),
+                                  out_at(0), lrep, static_cast<long long>(a.nh) * HD,
+                                  limit(0));
             }
         }
         if (i + 1 < len) {
