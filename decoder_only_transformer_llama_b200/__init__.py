@@ -603,41 +603,52 @@ def op_linear(A, W, out, stream=None, workspace=None):
 # A step's calls are a few microseconds of device time each, so their checks
 # are kept to a handful of attribute reads per tensor.
 
-_torch_module = None
+_torch_module = _cur_device = _raw_stream = None
 
 
 def _torch():
-    global _torch_module
+    """torch, imported on first use, with what a call asks of it every time."""
+    global _torch_module, _cur_device, _raw_stream
     if _torch_module is None:
         import torch
+        # what torch.cuda.current_device() and current_stream().cuda_stream wrap, a tenth of their time
+        _cur_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
         _torch_module = torch
     return _torch_module
 
 
-def _on(stream, torch, dev: int) -> int:
+def _on(stream, dev: int):
     """The stream's handle; None: the device's current stream."""
-    if stream is not None:
-        return stream.cuda_stream
-    try:
-        return torch._C._cuda_getCurrentRawStream(dev)     # what torch.cuda.current_stream() wraps, 40 times as fast
-    except AttributeError:
-        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(dev) if stream is None else stream.cuda_stream
 
 
-def _home(t, name: str, torch) -> int:
+def _home(t, name: str) -> int:
     """Device index of a call's first tensor, which must be the current CUDA device (the stream's)."""
     if not getattr(t, "is_cuda", False):
         raise ValueError(f"{name} must be a CUDA tensor")
-    if t.get_device() != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t.get_device()
+    dev = t.get_device()
+    if dev != _cur_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{_cur_device()}")
+    return dev
+
+
+def _refuse(t, dtype, want: str, name: str, dev: int):
+    raise ValueError(f"{name} must be a contiguous {dtype} tensor {want} on cuda:{dev}, not {t.dtype} {tuple(t.shape)} on "
+                     f"{t.device}" + ("" if t.is_contiguous() else ", strided"))
+
+
+def _vec(t, dtype, n: int, name: str, dev: int):
+    """Checks a contiguous tensor of n values of torch dtype `dtype` on device `dev`; returns its address."""
+    if t.numel() != n or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtype, f"of {n} values", name, dev)
+    return t.data_ptr()
 
 
 def _arg(t, dtype, shape, name: str, dev: int):
     """Checks a contiguous tensor of torch dtype `dtype` and shape `shape` on device `dev`; returns its address."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)} on cuda:{dev}, not "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}" + ("" if t.is_contiguous() else ", strided"))
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, dtype, f"of shape {tuple(shape)}", name, dev)
     return t.data_ptr()
 
 
@@ -645,10 +656,6 @@ def _table(t, rows: int, name: str, torch, dev: int):
     """Checks an int32 [rows, any] table; returns its address and width."""
     width = t.shape[1] if t.dim() == 2 else -1
     return _arg(t, torch.int32, (rows, width), name, dev), width
-
-
-def _status_arg(status, torch, dev: int):
-    return None if status is None else _arg(status, torch.int32, (1,), "status", dev)
 
 
 def paged_plan(ctx_lens, new_lens, block_tables, free_pages, free_count, page_size: int, seq_lens, cu_new, slots,
@@ -660,25 +667,28 @@ def paged_plan(ctx_lens, new_lens, block_tables, free_pages, free_count, page_si
     cu_new [B+1], positions [T], free_left [1]; int64 slots [T].  seq_lens may
     be ctx_lens and free_left may be free_count: the step then updates them."""
     torch = _torch()
-    dev = _home(ctx_lens, "ctx_lens", torch)
+    dev = _home(ctx_lens, "ctx_lens")
     i32 = torch.int32
     B, T, n = ctx_lens.numel(), slots.numel(), free_pages.numel()
     tables, width = _table(block_tables, B, "block_tables", torch, dev)
-    _check(_lib.llama_paged_plan(
-        _arg(ctx_lens, i32, (B,), "ctx_lens", dev), _arg(new_lens, i32, (B,), "new_lens", dev), B, page_size, tables,
-        width, _arg(free_pages, i32, (n,), "free_pages", dev), n, _arg(free_count, i32, (1,), "free_count", dev), T,
-        _arg(seq_lens, i32, (B,), "seq_lens", dev), _arg(cu_new, i32, (B + 1,), "cu_new", dev),
-        _arg(slots, torch.int64, (T,), "slots", dev), _arg(positions, i32, (T,), "positions", dev),
-        _arg(free_left, i32, (1,), "free_left", dev), _status_arg(status, torch, dev), _on(stream, torch, dev)))
+    rc = _lib.llama_paged_plan(
+        _vec(ctx_lens, i32, B, "ctx_lens", dev), _vec(new_lens, i32, B, "new_lens", dev), B, page_size, tables, width,
+        _vec(free_pages, i32, n, "free_pages", dev), n, _vec(free_count, i32, 1, "free_count", dev), T,
+        _vec(seq_lens, i32, B, "seq_lens", dev), _vec(cu_new, i32, B + 1, "cu_new", dev),
+        _vec(slots, torch.int64, T, "slots", dev), _vec(positions, i32, T, "positions", dev),
+        _vec(free_left, i32, 1, "free_left", dev), None if status is None else _vec(status, i32, 1, "status", dev),
+        _on(stream, dev))
+    if rc:
+        _check(rc)
 
 
 def rope_table(out, theta: float = 10000.0, stream=None):
     """Fills out, fp32 [len, head_dim/2, 2], with the rotation table that paged_append reads."""
     torch = _torch()
-    dev = _home(out, "out", torch)
+    dev = _home(out, "out")
     _need(out.dim() == 3 and out.shape[2] == 2, "out must be [len, head_dim/2, 2]")
     _check(_lib.llama_rope_table(_arg(out, torch.float32, out.shape, "out", dev), out.shape[0], 2 * out.shape[1],
-                                 float(theta), _on(stream, torch, dev)))
+                                 float(theta), _on(stream, dev)))
     return out
 
 
@@ -718,7 +728,7 @@ def paged_append(q, k, v, positions, slots, rope, q_out, k_pages, v_pages, q_nor
     are [T, heads, head_dim] views with any row stride, float32 or of the
     cache's dtype; positions int32 and slots int64 hold at least T entries."""
     torch = _torch()
-    dev = _home(q, "q", torch)
+    dev = _home(q, "q")
     dt, src, f32 = q_out.dtype, q.dtype, torch.float32
     kp, vp, (n_pages, nkv, page, hd) = _pools(k_pages, v_pages, dt, dev)
     _need(q.dim() == 3, "q must be [T, n_heads, head_dim]")
@@ -728,14 +738,17 @@ def paged_append(q, k, v, positions, slots, rope, q_out, k_pages, v_pages, q_nor
     _need(rope.dim() == 3, "rope must be [len, head_dim/2, 2]")
     (qp, qs), (kq, ks), (vq, vs) = (_rows(q, src, (T, nh, hd), "q", dev), _rows(k, src, (T, nkv, hd), "k", dev),
                                     _rows(v, src, (T, nkv, hd), "v", dev))
-    _check(_lib.llama_paged_append(
+    rc = _lib.llama_paged_append(
         qp, qs, kq, ks, vq, vs, _code(src, torch, "q"), T, nh, nkv, hd,
-        None if q_norm is None else _arg(q_norm, f32, (hd,), "q_norm", dev),
-        None if k_norm is None else _arg(k_norm, f32, (hd,), "k_norm", dev), eps,
+        None if q_norm is None else _vec(q_norm, f32, hd, "q_norm", dev),
+        None if k_norm is None else _vec(k_norm, f32, hd, "k_norm", dev), eps,
         _arg(rope, f32, (rope.shape[0], hd // 2, 2), "rope", dev), rope.shape[0],
-        _arg(positions, torch.int32, (n,), "positions", dev),
-        _arg(slots, torch.int64, (slots.numel(),), "slots", dev), _arg(q_out, dt, (T, nh, hd), "q_out", dev), kp, vp,
-        n_pages, page, _code(dt, torch, "q_out"), _status_arg(status, torch, dev), _on(stream, torch, dev)))
+        _vec(positions, torch.int32, n, "positions", dev),
+        _vec(slots, torch.int64, slots.numel(), "slots", dev), _arg(q_out, dt, (T, nh, hd), "q_out", dev), kp, vp,
+        n_pages, page, _code(dt, torch, "q_out"),
+        None if status is None else _vec(status, torch.int32, 1, "status", dev), _on(stream, dev))
+    if rc:
+        _check(rc)
     return q_out
 
 
@@ -760,7 +773,7 @@ def paged_attention(q, k_pages, v_pages, block_tables, cu_new, seq_lens, out, ma
     if None.  workspace: paged_attention_workspace(), kept by the caller; None
     makes a new one for this call."""
     torch = _torch()
-    dev = _home(q, "q", torch)
+    dev = _home(q, "q")
     dt, i32 = q.dtype, torch.int32
     kp, vp, (n_pages, nkv, page, hd) = _pools(k_pages, v_pages, dt, dev)
     _need(q.dim() == 3 and q.shape[2] == hd, "q must be [T, n_heads, head_dim] of the pages' head_dim")
@@ -773,12 +786,15 @@ def paged_attention(q, k_pages, v_pages, block_tables, cu_new, seq_lens, out, ma
         with torch.cuda.stream(stream if stream is not None else torch.cuda.current_stream()):
             workspace = paged_attention_workspace(q, nkv, max_new)
     ws_bytes = workspace.numel()
-    _check(_lib.llama_paged_attention(
+    rc = _lib.llama_paged_attention(
         _arg(q, dt, (T, nh, hd), "q", dev), kp, vp, _code(dt, torch, "q"), T, nh, nkv, hd, B,
-        _arg(cu_new, i32, (B + 1,), "cu_new", dev), _arg(seq_lens, i32, (B,), "seq_lens", dev), tables, width, n_pages,
+        _vec(cu_new, i32, B + 1, "cu_new", dev), _vec(seq_lens, i32, B, "seq_lens", dev), tables, width, n_pages,
         page, max_new, hd ** -0.5 if scale is None else scale, _arg(out, dt, (T, nh, hd), "out", dev),
-        _arg(workspace, torch.uint8, (ws_bytes,), "workspace", dev), ws_bytes, _status_arg(status, torch, dev),
-        _on(stream, torch, dev)))
+        _vec(workspace, torch.uint8, ws_bytes, "workspace", dev), ws_bytes,
+        None if status is None else _vec(status, torch.int32, 1, "status", dev),
+        _on(stream, dev))
+    if rc:
+        _check(rc)
     return out
 
 
@@ -787,14 +803,16 @@ def sample_rows(logits, temperature, uniforms, out, top_k=None, top_p=None, min_
     logits [B, V]; temperature, uniforms, top_p, min_p fp32 [B], top_k int32
     [B] (None: that filter is off); out int32 [B]."""
     torch = _torch()
-    dev = _home(logits, "logits", torch)
+    dev = _home(logits, "logits")
     f32, i32 = torch.float32, torch.int32
     _need(logits.dim() == 2, "logits must be [B, V]")
     B, V = logits.shape
-    _check(_lib.llama_sample_rows(
-        _arg(logits, f32, (B, V), "logits", dev), B, V, _arg(temperature, f32, (B,), "temperature", dev),
-        None if top_k is None else _arg(top_k, i32, (B,), "top_k", dev),
-        None if top_p is None else _arg(top_p, f32, (B,), "top_p", dev),
-        None if min_p is None else _arg(min_p, f32, (B,), "min_p", dev),
-        _arg(uniforms, f32, (B,), "uniforms", dev), _arg(out, i32, (B,), "out", dev), _on(stream, torch, dev)))
+    rc = _lib.llama_sample_rows(
+        _arg(logits, f32, (B, V), "logits", dev), B, V, _vec(temperature, f32, B, "temperature", dev),
+        None if top_k is None else _vec(top_k, i32, B, "top_k", dev),
+        None if top_p is None else _vec(top_p, f32, B, "top_p", dev),
+        None if min_p is None else _vec(min_p, f32, B, "min_p", dev),
+        _vec(uniforms, f32, B, "uniforms", dev), _vec(out, i32, B, "out", dev), _on(stream, dev))
+    if rc:
+        _check(rc)
     return out
