@@ -11,6 +11,10 @@ namespace llb {
 
 constexpr int kPagedMaxRequests = 1024;   // requests one call may hold (one thread of the plan kernel each)
 
+// Bytes at the start of a paged-attention workspace that hold arrival counters,
+// zero between launches; both kernels keep to them, so one workspace serves both.
+constexpr size_t kPagedCounters = 12288;
+
 struct PlanArgs {
     const int32_t* ctx_lens;
     const int32_t* new_lens;

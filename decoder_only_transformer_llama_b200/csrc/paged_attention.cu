@@ -21,8 +21,8 @@
 // scores and 16 HD / 128 outputs.
 //
 // A tile split between CTAs: each publishes its unnormalised (o, m, l) and
-// counts itself; the last to arrive merges all of them in CTA order (the same
-// bits from run to run; nobody waits) and clears the counter.
+// counts itself; the last to arrive merges, in CTA order (the same bits from run
+// to run; nobody waits), and clears the counter.
 #include <type_traits>
 
 #include "common.cuh"
@@ -42,7 +42,10 @@ constexpr int kMinUnits = 4;
 template <typename T> constexpr int kUnitKeys = sizeof(T) == 2 ? 64 : 32;
 
 // Workspace: counters, (m, l) and o of two partial tiles per CTA.
-constexpr size_t kOffMl = kMaxCtas * sizeof(int);
+constexpr int kFan = 8;                     // partial results merged at a time
+constexpr int kLevels = 3;                  // kFan^3 contributors: every CTA
+static_assert(kFan * kFan * kFan >= kMaxCtas && 2 * kLevels * kMaxCtas * sizeof(int) <= kPagedCounters, "merge tree");
+constexpr size_t kOffMl = kPagedCounters;
 constexpr size_t kOffO = kOffMl + 2ull * kMaxCtas * kRows * sizeof(float2);
 constexpr size_t ws_bytes(int hd) { return kOffO + 2ull * kMaxCtas * kRows * hd * sizeof(float); }
 
@@ -99,98 +102,62 @@ template <typename T> __device__ __forceinline__ bool not_finite16(uint32_t h) {
 }
 }  // namespace
 
-// The partial results of a tile's contributors cf .. cl (contributor x published
-// in slot 2 x, the first one in slot 2 cf + 1), merged in their order: per step
-// of at most `step` contributors their (m, l) into shared memory, the rows'
-// maxima and weights from there, then the outputs, a thread holding four
-// columns of a row with kDeep loads in flight.  Row r of the tile lies at
-// out + (r >> lrep) * token + (r & (2^lrep - 1)) * HD and sees lim0 + (r >> lrep) keys.
-
+// Merges the partial results of n <= kFan contributors of a tile, x = first, first
+// + stride, ... (contributor x's in slot 2 x, the tile's first one cf's in slot
+// 2 cf + 1), in their order.  A thread holds four columns of a row and asks for
+// everything it needs at once.  With `out` the rows are finished: row r of the
+// tile lies at out + (r >> lrep) * token + (r & (2^lrep - 1)) * HD and sees lim0 +
+// (r >> lrep) keys; without it the merged partial result takes the place of the
+// first one (a row's threads lie in one warp, so all have read it).
 template <typename T, int HD>
-__device__ __forceinline__ void merge_tile(const float2* part_ml, const float* part_o, int cf, int cl, int rows,
-                                        float2* s_ml, int step, T* out, int lrep, long long token, int lim0) {
-    constexpr int kMine = kRows * (HD / 4) / kThreads;
-    constexpr int kDeep = 8;
-    __shared__ float s_top[kRows], s_sum[kRows], s_corr[kRows];
-    const int tid = threadIdx.x;
-    auto slot_of = [&](int x) { return static_cast<long long>(2 * x + (x == cf ? 1 : 0)) * kRows; };
-    if (tid < kRows) { s_top[tid] = -INFINITY; s_sum[tid] = 0.f; }
-    float4 o[kMine];
+__device__ __forceinline__ void merge_tile(float2* part_ml, float* part_o, int cf, int first, int n, int stride, int rows,
+                                           T* out, int lrep, long long token, int lim0) {
+    auto slot_of = [&](int k) {
+        const int x = first + k * stride;
+        return static_cast<long long>(2 * x + (x == cf ? 1 : 0)) * kRows;
+    };
+#pragma unroll 2
+    for (int idx = threadIdx.x; idx < rows * (HD / 4); idx += kThreads) {
+        const int r = idx / (HD / 4), d = (idx % (HD / 4)) * 4;
+        float2 ml[kFan];
+        float4 v[kFan];
 #pragma unroll
-    for (int y = 0; y < kMine; ++y) o[y] = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int x0 = cf; x0 <= cl; x0 += step) {
-        const int nx = min(step, cl + 1 - x0);
-        __syncthreads();
-#pragma unroll 4
-        for (int i = tid; i < nx * kRows; i += kThreads) {
-            const int r = i % kRows;
-            if (r < rows) s_ml[i] = __ldcg(&part_ml[slot_of(x0 + i / kRows) + r]);
-        }
-        __syncthreads();
-        {
-            // eight threads a row
-            const int r = tid >> 3;
-            float M = s_top[r], L = 0.f;
-            const float before = M;
-            if (r < rows)
-                for (int x = tid & 7; x < nx; x += 8) M = fmaxf(M, s_ml[x * kRows + r].x);
-#pragma unroll
-            for (int e = 4; e > 0; e >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, e));
-            const float Ms = M == -INFINITY ? 0.f : M;
-            if (r < rows)
-                for (int x = tid & 7; x < nx; x += 8) {
-                    const float2 ml = s_ml[x * kRows + r];
-                    const float f = ex2(ml.x - Ms);
-                    L += ml.y * f;
-                    s_ml[x * kRows + r].x = f;
-                }
-#pragma unroll
-            for (int e = 4; e > 0; e >>= 1) L += __shfl_xor_sync(0xffffffffu, L, e);
-            if ((tid & 7) == 0) {
-                const float corr = ex2(before - Ms);
-                s_corr[r] = corr;
-                s_sum[r] = s_sum[r] * corr + L;
-                s_top[r] = M;
+        for (int k = 0; k < kFan; ++k) {
+            ml[k] = make_float2(-INFINITY, 0.f);
+            v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (k < n) {
+                ml[k] = __ldcg(part_ml + slot_of(k) + r);
+                v[k] = __ldcg(reinterpret_cast<const float4*>(part_o + (slot_of(k) + r) * HD + d));
             }
         }
-        __syncthreads();
+        float M = -INFINITY, L = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int y = 0; y < kMine; ++y) {
-            const int idx = tid + y * kThreads, r = idx / (HD / 4), d = (idx % (HD / 4)) * 4;
-            if (r >= rows) break;
-            const float corr = s_corr[r];
-            o[y].x *= corr; o[y].y *= corr; o[y].z *= corr; o[y].w *= corr;
-#pragma unroll 1
-            for (int x = 0; x < nx; x += kDeep) {
-                float4 v[kDeep];
+        for (int k = 0; k < kFan; ++k) M = fmaxf(M, ml[k].x);
+        const float Ms = M == -INFINITY ? 0.f : M;
 #pragma unroll
-                for (int z = 0; z < kDeep; ++z)
-                    if (x + z < nx) v[z] = __ldcg(reinterpret_cast<const float4*>(part_o + (slot_of(x0 + x + z) + r) * HD + d));
-#pragma unroll
-                for (int z = 0; z < kDeep; ++z) {
-                    if (x + z >= nx) break;
-                    const float f = s_ml[(x + z) * kRows + r].x;
-                    o[y].x = fmaf(v[z].x, f, o[y].x); o[y].y = fmaf(v[z].y, f, o[y].y);
-                    o[y].z = fmaf(v[z].z, f, o[y].z); o[y].w = fmaf(v[z].w, f, o[y].w);
-                }
-            }
+        for (int k = 0; k < kFan; ++k) {
+            if (k >= n) break;
+            const float f = ex2(ml[k].x - Ms);
+            L += ml[k].y * f;
+            o.x = fmaf(v[k].x, f, o.x); o.y = fmaf(v[k].y, f, o.y);
+            o.z = fmaf(v[k].z, f, o.z); o.w = fmaf(v[k].w, f, o.w);
         }
-    }
-#pragma unroll
-    for (int y = 0; y < kMine; ++y) {
-        const int idx = tid + y * kThreads, r = idx / (HD / 4), d = (idx % (HD / 4)) * 4;
-        if (r >= rows) break;
-        const float L = s_sum[r];
+        if (!out) {
+            *reinterpret_cast<float4*>(part_o + (slot_of(0) + r) * HD + d) = o;
+            if (d == 0) part_ml[slot_of(0) + r] = make_float2(M, L);
+            continue;
+        }
         T* dst = out + (r >> lrep) * token + (r & ((1 << lrep) - 1)) * HD + d;
-        const float4 v = lim0 + (r >> lrep) > 0 ? make_float4(o[y].x / L, o[y].y / L, o[y].z / L, o[y].w / L)
+        const float4 y = lim0 + (r >> lrep) > 0 ? make_float4(o.x / L, o.y / L, o.z / L, o.w / L)
                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
         if constexpr (sizeof(T) == 2) {
             uint2 w;
-            w.x = pack2<T>(v.x, v.y);
-            w.y = pack2<T>(v.z, v.w);
+            w.x = pack2<T>(y.x, y.y);
+            w.y = pack2<T>(y.z, y.w);
             *reinterpret_cast<uint2*>(dst) = w;
         } else {
-            *reinterpret_cast<float4*>(dst) = v;
+            *reinterpret_cast<float4*>(dst) = y;
         }
     }
 }
@@ -611,19 +578,33 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
             }
         }
         if (!whole) {
-            __threadfence();
-            __syncthreads();
-            if (tid == 0) {
-                const int seen = atomicAdd(counters + cf, 1);
-                s_last = seen == cl - cf;
-                if (s_last) counters[cf] = 0;
-            }
-            __syncthreads();
-            if (s_last) {
+            // A tree of groups of kFan: the last of a group to arrive merges it and
+            // goes on as its first member; one SM alone would read many partial
+            // results from L2 too slowly (few tiles over a long cache: 37
+            // contributors of 8 rows took 9 us in one go).
+            const int n = cl - cf + 1;
+            int k = c - cf, stride = 1;
+            for (int* level = counters;; level += 2 * kMaxCtas) {
+                const int first = k / (kFan * stride) * (kFan * stride);
+                const int members = min(kFan, (n - first + stride - 1) / stride);
+                const int x = cf + first;
                 __threadfence();
-                merge_tile<T, HD>(part_ml, part_o, cf, cl, rows, reinterpret_cast<float2*>(scr), SCR / (kRows * 8),
-                                  out_at(0), lrep, static_cast<long long>(a.nh) * HD,
-                                  limit(0));
+                __syncthreads();
+                if (tid == 0) {
+                    int* counter = level + 2 * x + (first == 0 ? 1 : 0);
+                    s_last = atomicAdd(counter, 1) == members - 1;
+                    if (s_last) *counter = 0;
+                }
+                __syncthreads();
+                if (!s_last) break;
+                __threadfence();
+                const bool top = n <= kFan * stride;
+                if (top || members > 1)
+                    merge_tile<T, HD>(part_ml, part_o, cf, x, members, stride, rows, top ? out_at(0) : nullptr, lrep,
+                                      static_cast<long long>(a.nh) * HD, limit(0));
+                if (top) break;
+                k = first;
+                stride *= kFan;
             }
         }
         if (i + 1 < len) {

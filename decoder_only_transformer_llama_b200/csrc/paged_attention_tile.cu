@@ -48,7 +48,8 @@ constexpr int kMinUnits = 2;
 constexpr int kMaxSlots = 8;
 constexpr uint32_t kColS = 0, kColO = 256;  // S_t at kColS + 128 t, O_t at kColO + 128 t
 
-constexpr size_t kOffMl = 4096;             // counters: two per CTA
+static_assert(2 * kMaxCtas * sizeof(int) <= kPagedCounters, "two counters per CTA");
+constexpr size_t kOffMl = kPagedCounters;
 constexpr size_t kOffO = kOffMl + 2ull * kMaxCtas * kRows * sizeof(float2);
 constexpr size_t ws_bytes(int hd) { return kOffO + 2ull * kMaxCtas * kRows * hd * sizeof(float); }
 

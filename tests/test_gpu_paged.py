@@ -403,6 +403,30 @@ def test_attention_bad_tables_and_offsets(llb, dtype, hd, max_new):
     assert ((got[0] - want[0]).abs() <= tol[0]).all()
 
 
+def test_attention_one_workspace_for_every_call(llb):
+    """One workspace, sized for the longest chunk, serves calls of every kind in turn: long caches split over many
+    CTAs, chunks on the tile kernel, short ones again."""
+    g = torch.Generator().manual_seed(12)
+    page, nkv, nh, hd, dt = 64, 1, 8, 128, torch.bfloat16
+    jobs = [([1], [20000]), ([300], [2000]), ([1], [20001]), ([2, 200], [9000, 200]), ([1, 1], [5, 15000])]
+    ws = None
+    for new, seqs in jobs + jobs[::-1]:
+        pools, tables, dense = paged_cache(seqs, page, nkv, hd, dt, g)
+        q = torch.randn(sum(new), nh, hd, generator=g).to(dt)
+        if ws is None:
+            ws = llb.paged_attention_workspace(q.cuda(), nkv, 300)
+        out = torch.empty(sum(new), nh, hd, dtype=dt, device="cuda")
+        cu = [0] + torch.tensor(new).cumsum(0).tolist()
+        llb.paged_attention(q.cuda(), pools[0].cuda(), pools[1].cuda(), tables.cuda(), i32(cu), i32(seqs), out,
+                            max_new=max(new), workspace=ws)
+        got = out.cpu().double()
+        for b, n in enumerate(new):
+            rows = sorted({0, n // 2, n - 1})            # the 64-bit attention of three rows of each request
+            for i in rows:
+                want, tol = R.attention(q[cu[b] + i:cu[b] + i + 1], *dense[b], 1, seqs[b] - n + i + 1, hd ** -0.5)
+                assert ((got[cu[b] + i] - want[0]).abs() <= tol[0]).all(), (new, seqs, b, i)
+
+
 def test_attention_on_two_streams_and_in_graphs(llb):
     """Two captured calls with a workspace each, replayed at once on two streams beside eager calls."""
     g = torch.Generator().manual_seed(6)
