@@ -44,11 +44,15 @@ constexpr int kRows = 256;
 constexpr int kKeys = 128;
 constexpr int kBox = 128 * 128;             // 128 rows of 64 16-bit values
 constexpr int kMaxCtas = 160;
-constexpr int kMinUnits = 2;
+// Units per CTA below which fewer CTAs run: a unit takes about 2 us, a publish
+// and a merge of a split tile 5.
+constexpr int kMinUnits = 4;
+constexpr int kFan = 4;                     // partial results merged at a time
+constexpr int kLevels = 4;                  // kFan^4 contributors: every CTA
 constexpr int kMaxSlots = 8;
 constexpr uint32_t kColS = 0, kColO = 256;  // S_t at kColS + 128 t, O_t at kColO + 128 t
 
-static_assert(2 * kMaxCtas * sizeof(int) <= kPagedCounters, "two counters per CTA");
+static_assert(kFan * kFan * kFan * kFan >= kMaxCtas && 4 * kLevels * kMaxCtas * sizeof(int) <= kPagedCounters, "merge tree");
 constexpr size_t kOffMl = kPagedCounters;
 constexpr size_t kOffO = kOffMl + 2ull * kMaxCtas * kRows * sizeof(float2);
 constexpr size_t ws_bytes(int hd) { return kOffO + 2ull * kMaxCtas * kRows * hd * sizeof(float); }
@@ -134,6 +138,72 @@ __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
 template <typename T> __device__ __forceinline__ bool not_finite16(uint32_t h) {
     constexpr uint32_t e = std::is_same<T, bf16>::value ? 0x7f80u : 0x7c00u;
     return (h & e) == e;
+}
+
+// Merges the partial results of sub-tile t of n <= kFan contributors of a tile, x =
+// first, first + stride, ... (contributor x's in slot 2 x, the tile's first one
+// cf's in slot 2 cf + 1), in their order: rows_live rows, spread over the 128
+// threads with as many columns of a row side by side as there is room for.
+// With `out` the rows are finished: row r lies at out + (r >> lrep) * token + (r &
+// (2^lrep - 1)) * HD and sees lim0 + (r >> lrep) keys; without it the merged
+// partial result takes the place of the first one.
+template <typename T, int HD>
+__device__ __noinline__ void merge_half(float2* part_ml, float4* part_o, int cf, int first, int n, int stride, int t,
+                                        int rows_live, T* out, int lrep, long long token, int lim0) {
+    const int tid = threadIdx.x & 127;
+    const int lr = rows_live > 1 ? 32 - __clz(rows_live - 1) : 0;    // rows side by side: 2^lr
+    const int r = tid & ((1 << lr) - 1), row = t * 128 + r;
+    const bool in = r < rows_live;
+    long long slot[kFan];
+    float f[kFan];
+    float M = -INFINITY, L = 0.f;
+    float2 ml[kFan];
+#pragma unroll
+    for (int k = 0; k < kFan; ++k) {
+        const int x = first + (k < n ? k : 0) * stride;
+        slot[k] = static_cast<long long>(2 * x + (x == cf ? 1 : 0)) * kRows;
+        ml[k] = in ? __ldcg(part_ml + slot[k] + row) : make_float2(-INFINITY, 0.f);
+    }
+#pragma unroll
+    for (int k = 0; k < kFan; ++k)
+        if (k < n) M = fmaxf(M, ml[k].x);
+    const float Ms = M == -INFINITY ? 0.f : M;
+#pragma unroll
+    for (int k = 0; k < kFan; ++k) {
+        f[k] = k < n ? ex2(ml[k].x - Ms) : 0.f;
+        if (k < n) L += ml[k].y * f[k];
+    }
+    T* dst = out ? out + (r >> lrep) * token + (r & ((1 << lrep) - 1)) * HD : nullptr;
+    const bool some = lim0 + (r >> lrep) > 0;
+    if (in) {
+#pragma unroll 4
+        for (int d = tid >> lr; d < HD / 4; d += 128 >> lr) {
+            float4 v[kFan];
+#pragma unroll
+            for (int k = 0; k < kFan; ++k)
+                if (k < n) v[k] = __ldcg(part_o + slot[k] * (HD / 4) + static_cast<long long>(d) * kRows + row);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kFan; ++k) {
+                if (k >= n) break;
+                o.x = fmaf(v[k].x, f[k], o.x); o.y = fmaf(v[k].y, f[k], o.y);
+                o.z = fmaf(v[k].z, f[k], o.z); o.w = fmaf(v[k].w, f[k], o.w);
+            }
+            if (out) {
+                const float inv = some ? 1.f / L : 0.f;
+                uint2 w;
+                w.x = some ? pack2<T>(o.x * inv, o.y * inv) : 0u;
+                w.y = some ? pack2<T>(o.z * inv, o.w * inv) : 0u;
+                *reinterpret_cast<uint2*>(dst + 4 * d) = w;
+            } else {
+                part_o[slot[0] * (HD / 4) + static_cast<long long>(d) * kRows + row] = o;
+            }
+        }
+    }
+    if (!out) {
+        named_sync(1 + t, 128);                    // every thread has read the first one's (m, l)
+        if (in && tid >> lr == 0) part_ml[slot[0] + row] = make_float2(M, L);
+    }
 }
 
 // A part of one tile that a CTA works on: units c.j .. c.j + len - 1.
@@ -532,49 +602,32 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
                     }
                 }
                 if (!whole) {
-                    __threadfence();
-                    named_sync(1 + t, 128);
-                    if (r == 0) {
-                        const int seen = atomicAdd(counters + 2 * cf + t, 1);
-                        s_last[t] = seen == cl - cf;
-                        if (s_last[t]) counters[2 * cf + t] = 0;
-                    }
-                    named_sync(1 + t, 128);
-                    if (s_last[t] && live) {
+                    // a tree of groups of kFan, as in the kernel of short tiles
+                    const int n = cl - cf + 1, rows_live = min(128, (rq.n - t0 - t * half) << lrep);
+                    T* first_row = static_cast<T*>(a.out) +
+                                   (static_cast<long long>(rq.q0 + t0 + t * half) * a.nh + sg.c.g * rep) * HD;
+                    int k = cta - cf, stride = 1;
+                    for (int* level = counters;; level += 4 * kMaxCtas) {
+                        const int first = k / (kFan * stride) * (kFan * stride);
+                        const int members = min(kFan, (n - first + stride - 1) / stride);
+                        const int x = cf + first;
                         __threadfence();
-                        float M = -INFINITY, L = 0.f;
-                        for (int x = cf; x <= cl; ++x)
-                            M = fmaxf(M, __ldcg(&part_ml[static_cast<long long>(2 * x + (x == cf)) * kRows + row].x));
-                        const float Ms = M == -INFINITY ? 0.f : M;
-                        for (int x = cf; x <= cl; ++x) {
-                            const float2 ml = __ldcg(part_ml + static_cast<long long>(2 * x + (x == cf)) * kRows + row);
-                            L += ml.y * ex2(ml.x - Ms);
+                        named_sync(1 + t, 128);
+                        if (r == 0) {
+                            int* counter = level + 2 * (2 * x + (first == 0 ? 1 : 0)) + t;
+                            s_last[t] = atomicAdd(counter, 1) == members - 1;
+                            if (s_last[t]) *counter = 0;
                         }
-#pragma unroll 1
-                        for (int d = 0; d < HD / 4; d += 4) {
-                            float4 o[4];
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-                            for (int x = cf; x <= cl; ++x) {
-                                const long long b = static_cast<long long>(2 * x + (x == cf)) * kRows;
-                                const float f = ex2(__ldcg(&part_ml[b + row].x) - Ms);
-#pragma unroll
-                                for (int e = 0; e < 4; ++e) {
-                                    const float4 v = __ldcg(part_o + b * (HD / 4) + static_cast<long long>(d + e) * kRows + row);
-                                    o[e].x += v.x * f; o[e].y += v.y * f; o[e].z += v.z * f; o[e].w += v.w * f;
-                                }
-                            }
-                            const float iL = 1.f / L;
-                            uint4 w[2];
-                            uint32_t* pw = reinterpret_cast<uint32_t*>(w);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                pw[2 * e] = lim > 0 ? pack2<T>(o[e].x * iL, o[e].y * iL) : 0u;
-                                pw[2 * e + 1] = lim > 0 ? pack2<T>(o[e].z * iL, o[e].w * iL) : 0u;
-                            }
-                            reinterpret_cast<uint4*>(dst + 4 * d)[0] = w[0];
-                            reinterpret_cast<uint4*>(dst + 4 * d)[1] = w[1];
-                        }
+                        named_sync(1 + t, 128);
+                        if (!s_last[t]) break;
+                        __threadfence();
+                        const bool top = n <= kFan * stride;
+                        if (top || members > 1)
+                            merge_half<T, HD>(part_ml, part_o, cf, x, members, stride, t, rows_live, top ? first_row : nullptr,
+                                              lrep, static_cast<long long>(a.nh) * HD, rq.seq - rq.n + t0 + t * half + 1);
+                        if (top) break;
+                        k = first;
+                        stride *= kFan;
                     }
                     named_sync(1 + t, 128);        // s_last is free again
                 }
