@@ -171,6 +171,10 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
     constexpr int CPR = ROW / 16;                 // 16-byte chunks per row
     constexpr int RPP = kThreads / CPR;           // rows one pass of the CTA copies
     constexpr int NPG = KU / 16;                  // most pages of a unit
+    // P is rounded to the cache's type for the second product (relative to P at most
+    // half a step, of the size of the output's own rounding; l sums it unrounded).
+    // fp16 loses relative precision below 2^-14: all weights carry a factor 2^8 there.
+    constexpr float kLift = std::is_same<T, f16>::value ? 8.f : 0.f;
     extern __shared__ __align__(128) uint8_t smem[];
     // ring | scratch (16-bit: o of 4 warps x 4 rows; fp32: q, scores) | work list
     constexpr int SCR = H16 ? 4 * 4 * HD * 4 : kRows * HD * 4 + kRows * KU * 4;
@@ -191,6 +195,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
     if (c >= P) return;
     const long long u0 = run_start(c, W, P), u1 = run_start(c + 1, W, P);
     const int len = static_cast<int>(u1 - u0);
+    WorkCur ic = work_at(shape, req, cum, a.B, a.nkv, u0);   // the next unit to copy
     const int rep = a.nh / a.nkv, lrep = 4 - shape.lr;      // 16 rows = 2^lr tokens * rep heads
     const int R = 1 << shape.lr;
 
@@ -201,7 +206,6 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
     const T* vp = static_cast<const T*>(a.v_pages);
 
     // ---- copies: the cursor of the next unit to issue, its tile's last key and its pages
-    WorkCur ic = work_at(shape, req, cum, a.B, a.nkv, u0);
     int pg[NPG], ikend = 0;
     const int32_t* itable = nullptr;
     auto issue_tile = [&]() {
@@ -398,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 2) paged_attn_kernel(PagedAttnArgs a
                 const float corr = ex2(m2[x] - ms);
                 float p[4], rs = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e) { p[e] = ex2(s[e] - ms); rs += p[e]; }
+                for (int e = 0; e < 4; ++e) { p[e] = ex2(s[e] - (ms - kLift)); rs += p[e]; }
                 l2[x] = l2[x] * corr + rs;        // this lane's keys; summed over the quad at the end
                 m2[x] = mn;
                 pa[x] = pack2<T>(p[0], p[1]);
@@ -660,10 +664,15 @@ static int attn_hd(const PagedAttnArgs& a, cudaStream_t st) {
     return attn_go<T, 128>(a, st);
 }
 
-// Chunks take the tile kernel when a request's rows per KV head fill more than
-// two 16-row tiles (16-bit caches, head_dim 64 or 128).
+// A call takes the tile kernel when the longest chunk's rows per KV head fill
+// more than one 16-row tile (16-bit caches, head_dim 64 or 128).  Measured both
+// ways, 8 KV heads, head_dim 128, tile kernel / 16-row kernel, us: 8 tokens of 4
+// heads each, 1 request over 300 keys 14 / 19, over 4000 23 / 32, 16 requests over
+// 4000 71 / 88; 64 tokens 17 / 25, 38 / 52, 95 / 567.  At 16 rows the 16-row
+// kernel is the faster one where there is much to read (4 tokens, 16 requests
+// over 4000 keys: 69 / 59), the slower one where there is little (15 / 22).
 static bool tile_shape(int nh, int nkv, int hd, int dtype, int max_new) {
-    return dtype != LLAMA_F32 && hd != 32 && static_cast<long long>(max_new) * (nh / nkv) > 2 * kRows;
+    return dtype != LLAMA_F32 && hd != 32 && static_cast<long long>(max_new) * (nh / nkv) > kRows;
 }
 
 size_t paged_attention_ws(int nh, int nkv, int hd, int dtype, int max_new) {

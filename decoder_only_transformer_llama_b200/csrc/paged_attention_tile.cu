@@ -10,7 +10,9 @@
 //   S_t = Q_t K^T  tcgen05, 128 x 128 over head_dim, from swizzled TMA tiles
 //   softmax        one thread per row: scores by tcgen05.ld, running maximum m
 //                  and sum l in registers in the log2 domain, P = 2^(s - m)
-//                  rounded to 16 bits over the first half of S_t's columns
+//                  rounded to 16 bits (half a step of P, the size of the
+//                  output's own rounding; l sums it unrounded) over the first
+//                  half of S_t's columns
 //   O_t += P_t V   tcgen05 with P_t from TMEM and V read MN-major from its tile
 // The two sub-tiles alternate on the tensor core: while one's softmax runs,
 // the other's products do.  MMAs of one thread run in order, so S_t of the next
@@ -47,6 +49,7 @@ constexpr int kMaxCtas = 160;
 // Units per CTA below which fewer CTAs run: a unit takes about 2 us, a publish
 // and a merge of a split tile 5.
 constexpr int kMinUnits = 4;
+constexpr int kWhole = 5;                   // tiles of so many units stay whole
 constexpr int kFan = 4;                     // partial results merged at a time
 constexpr int kLevels = 4;                  // kFan^4 contributors: every CTA
 constexpr int kMaxSlots = 8;
@@ -176,27 +179,35 @@ __device__ __noinline__ void merge_half(float2* part_ml, float4* part_o, int cf,
     T* dst = out ? out + (r >> lrep) * token + (r & ((1 << lrep) - 1)) * HD : nullptr;
     const bool some = lim0 + (r >> lrep) > 0;
     if (in) {
-#pragma unroll 4
-        for (int d = tid >> lr; d < HD / 4; d += 128 >> lr) {
-            float4 v[kFan];
+#pragma unroll 2
+        for (int d = 2 * (tid >> lr); d < HD / 4; d += 256 >> lr) {      // eight columns
+            float4 v[kFan][2];
 #pragma unroll
             for (int k = 0; k < kFan; ++k)
-                if (k < n) v[k] = __ldcg(part_o + slot[k] * (HD / 4) + static_cast<long long>(d) * kRows + row);
-            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (k < n)
 #pragma unroll
-            for (int k = 0; k < kFan; ++k) {
-                if (k >= n) break;
-                o.x = fmaf(v[k].x, f[k], o.x); o.y = fmaf(v[k].y, f[k], o.y);
-                o.z = fmaf(v[k].z, f[k], o.z); o.w = fmaf(v[k].w, f[k], o.w);
+                    for (int e = 0; e < 2; ++e)
+                        v[k][e] = __ldcg(part_o + slot[k] * (HD / 4) + static_cast<long long>(d + e) * kRows + row);
+            float4 o[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                for (int k = 0; k < kFan; ++k) {
+                    if (k >= n) break;
+                    o[e].x = fmaf(v[k][e].x, f[k], o[e].x); o[e].y = fmaf(v[k][e].y, f[k], o[e].y);
+                    o[e].z = fmaf(v[k][e].z, f[k], o[e].z); o[e].w = fmaf(v[k][e].w, f[k], o[e].w);
+                }
+                if (!out) part_o[slot[0] * (HD / 4) + static_cast<long long>(d + e) * kRows + row] = o[e];
             }
             if (out) {
                 const float inv = some ? 1.f / L : 0.f;
-                uint2 w;
-                w.x = some ? pack2<T>(o.x * inv, o.y * inv) : 0u;
-                w.y = some ? pack2<T>(o.z * inv, o.w * inv) : 0u;
-                *reinterpret_cast<uint2*>(dst + 4 * d) = w;
-            } else {
-                part_o[slot[0] * (HD / 4) + static_cast<long long>(d) * kRows + row] = o;
+                uint4 w = make_uint4(0u, 0u, 0u, 0u);
+                if (some) {
+                    w.x = pack2<T>(o[0].x * inv, o[0].y * inv); w.y = pack2<T>(o[0].z * inv, o[0].w * inv);
+                    w.z = pack2<T>(o[1].x * inv, o[1].y * inv); w.w = pack2<T>(o[1].z * inv, o[1].w * inv);
+                }
+                *reinterpret_cast<uint4*>(dst + 4 * d) = w;
             }
         }
     }
@@ -218,6 +229,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
                        const __grid_constant__ CUtensorMap mapV, PagedAttnArgs a, TileShape shape, int nslots) {
     constexpr int NB = HD / 64;                    // boxes per tile
+    // fp16 loses relative precision below 2^-14: weights, up to 2^8 before m moves,
+    // carry a factor 2^7 there
+    constexpr float kLift = std::is_same<T, f16>::value ? 7.f : 0.f;
     constexpr int TILE = NB * kBox;                // a [128][HD] tile
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -239,7 +253,10 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
     const long long parts = max((W + kMinUnits - 1) / kMinUnits, min(s_tiles, W));
     const int P = static_cast<int>(parts < gridDim.x ? parts : gridDim.x), cta = blockIdx.x;
     if (cta >= P) return;                          // the whole CTA, before any barrier or TMEM
-    const long long u0 = run_start(cta, W, P), u1 = run_start(cta + 1, W, P);
+    WorkCur start, end;
+    const long long u0 = run_bound(shape, req, cum, a.B, a.nkv, run_start(cta, W, P), kWhole, start);
+    const long long u1 = run_bound(shape, req, cum, a.B, a.nkv, run_start(cta + 1, W, P), kWhole, end);
+    if (u1 <= u0) return;                          // a run inside a tile that its neighbours take
     const int rep = a.nh / a.nkv, lrep = 8 - shape.lr;
     const int half = 128 >> lrep;                  // tokens of a sub-tile
 
@@ -265,7 +282,7 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
     // every role walks the same segments
     auto first_segment = [&]() {
         Segment s;
-        s.c = work_at(shape, req, cum, a.B, a.nkv, u0);
+        s.c = start;
         s.len = static_cast<int>(min(static_cast<long long>(s.c.nu - s.c.j), u1 - u0));
         return s;
     };
@@ -518,7 +535,7 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
                         }
                     }
                     const float ms = m == -INFINITY ? 0.f : m;       // no key so far: every weight is 0
-                    const uint64_t scale2 = pk2(sl2, sl2), minus2 = pk2(-ms, -ms);
+                    const uint64_t scale2 = pk2(sl2, sl2), minus2 = pk2(kLift - ms, kLift - ms);
                     uint64_t sum2[2] = {pk2(0.f, 0.f), pk2(0.f, 0.f)};
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {

@@ -6,7 +6,8 @@
 // min((i + 1) R, n) - 1, i.e. units_of(i) units of K = 2^lk keys.  Units are
 // numbered by (request, head, tile, unit); CTA c of P takes the run [c W / P,
 // (c + 1) W / P), whatever the mix of lengths, and splits a tile between CTAs
-// where its run starts or ends inside it.
+// where its run starts or ends inside it.  Where a split costs more than a tile's
+// few units, run_bound moves such a boundary to the nearer end of the tile.
 #pragma once
 
 #include "common.cuh"
@@ -78,6 +79,61 @@ struct WorkCur {
     int b, g, tile, j, nu;   // request, KV head, tile, unit of it and the tile's units
 };
 
+__host__ __device__ __forceinline__ int ctx_of(const WorkReq& r) { return r.seq > r.n ? r.seq - r.n : 0; }
+
+__host__ __device__ __forceinline__ WorkCur work_at(TileShape s, const WorkReq* req, const long long* cum, int B, int nkv,
+                                           long long u) {
+    int lo = 0, hi = B - 1;          // the last request with cum <= u
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (cum[mid] <= u) lo = mid; else hi = mid - 1;
+    }
+    const WorkReq r = req[lo];
+    const long long per = request_units(s, ctx_of(r), r.n);
+    const long long rem = u - cum[lo];
+    WorkCur c;
+    c.b = lo;
+    c.g = rem <= 0xffffffffLL && per <= 0xffffffffLL ? static_cast<uint32_t>(rem) / static_cast<uint32_t>(per)
+                                                     : static_cast<int>(rem / per);
+    const long long v = rem - c.g * per;
+    c.tile = tile_at(s, ctx_of(r), r.n, v);
+    c.j = static_cast<int>(v - tiles_units(s, ctx_of(r), c.tile));
+    c.nu = units_of(s, ctx_of(r), r.n, c.tile);
+    return c;
+}
+
+// The first unit of the tile after c's (b == B behind the last one).
+__host__ __device__ __forceinline__ void next_tile(TileShape s, const WorkReq* req, int B, int nkv, WorkCur& c) {
+    c.j = 0;
+    if (++c.tile >= tiles_of(s, req[c.b].n)) {
+        c.tile = 0;
+        if (++c.g >= nkv) {
+            c.g = 0;
+            do { ++c.b; } while (c.b < B && req[c.b].n <= 0);
+            if (c.b >= B) return;
+        }
+    }
+    const WorkReq r = req[c.b];
+    c.nu = units_of(s, ctx_of(r), r.n, c.tile);
+}
+
+// The run boundary at unit u (0 .. W), moved to the nearer end of its tile if
+// that has at most `most` units, with the place it lies at (undefined at W).
+__host__ __device__ __forceinline__ long long run_bound(TileShape s, const WorkReq* req, const long long* cum, int B,
+                                                        int nkv, long long u, int most, WorkCur& at) {
+    if (u >= cum[B]) return cum[B];
+    at = work_at(s, req, cum, B, nkv, u);
+    if (at.j == 0 || at.nu > most) return u;
+    if (2 * at.j < at.nu) {
+        u -= at.j;
+        at.j = 0;
+    } else {
+        u += at.nu - at.j;
+        next_tile(s, req, B, nkv, at);
+    }
+    return u;
+}
+
 #ifdef __CUDACC__
 // Fills req[0 .. B) and cum[0 .. B] (units before each request) from the
 // call's offsets and lengths, with the checks of the entry point; CTA 0
@@ -129,43 +185,6 @@ __device__ __forceinline__ void build_work(const int32_t* cu, const int32_t* seq
     __syncthreads();
 }
 
-__device__ __forceinline__ int ctx_of(const WorkReq& r) { return r.seq > r.n ? r.seq - r.n : 0; }
-
-__device__ __forceinline__ WorkCur work_at(TileShape s, const WorkReq* req, const long long* cum, int B, int nkv,
-                                           long long u) {
-    int lo = 0, hi = B - 1;          // the last request with cum <= u
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (cum[mid] <= u) lo = mid; else hi = mid - 1;
-    }
-    const WorkReq r = req[lo];
-    const long long per = request_units(s, ctx_of(r), r.n);
-    const long long rem = u - cum[lo];
-    WorkCur c;
-    c.b = lo;
-    c.g = rem <= 0xffffffffLL && per <= 0xffffffffLL ? static_cast<uint32_t>(rem) / static_cast<uint32_t>(per)
-                                                     : static_cast<int>(rem / per);
-    const long long v = rem - c.g * per;
-    c.tile = tile_at(s, ctx_of(r), r.n, v);
-    c.j = static_cast<int>(v - tiles_units(s, ctx_of(r), c.tile));
-    c.nu = units_of(s, ctx_of(r), r.n, c.tile);
-    return c;
-}
-
-// The first unit of the tile after c's (b == B behind the last one).
-__device__ __forceinline__ void next_tile(TileShape s, const WorkReq* req, int B, int nkv, WorkCur& c) {
-    c.j = 0;
-    if (++c.tile >= tiles_of(s, req[c.b].n)) {
-        c.tile = 0;
-        if (++c.g >= nkv) {
-            c.g = 0;
-            do { ++c.b; } while (c.b < B && req[c.b].n <= 0);
-            if (c.b >= B) return;
-        }
-    }
-    const WorkReq r = req[c.b];
-    c.nu = units_of(s, ctx_of(r), r.n, c.tile);
-}
 #endif
 
 }  // namespace llb

@@ -55,6 +55,55 @@ int main() {
         }
         CHECK(prev == W);
     }
+    // whole walks: random requests, every CTA's run between its moved boundaries
+    for (int rnd = 0; rnd < 600; ++rnd) {
+        const int B = 1 + rand() % 12, nkv = 1 << rand() % 3, lk = 5 + rand() % 3, lr = 1 + rand() % 8;
+        const int most = rand() % 2 ? 4 : rand() % 9;
+        const TileShape s = {lr, lk};
+        WorkReq req[12];
+        long long cum[13] = {0};
+        for (int b = 0; b < B; ++b) {
+            const int n = rand() % 4 ? rand() % (rnd % 3 ? 60 : 900) : rand() % 2;
+            req[b].q0 = 0;
+            req[b].n = n;
+            req[b].seq = rand() % 7 ? n + rand() % (rnd % 5 ? 300 : 4000) : rand() % (n + 1);
+            cum[b + 1] = cum[b] + request_units(s, ctx_of(req[b]), n) * nkv;
+        }
+        const long long W = cum[B];
+        if (W == 0) continue;
+        const long long P = 1 + rand() % (W < 300 ? W : 300);
+        long long prev = 0;
+        for (int c = 0; c < P; ++c) {
+            WorkCur at, end;
+            const long long u0 = run_bound(s, req, cum, B, nkv, run_start(c, W, P), most, at);
+            const long long u1 = run_bound(s, req, cum, B, nkv, run_start(c + 1, W, P), most, end);
+            CHECK(u0 == prev && u1 >= u0);
+            prev = u1;
+            WorkCur w = at;
+            for (long long u = u0; u < u1;) {
+                // the place reached by walking is the place found by searching
+                const WorkCur f = work_at(s, req, cum, B, nkv, u);
+                CHECK(f.b == w.b && f.g == w.g && f.tile == w.tile && f.j == w.j && f.nu == w.nu);
+                const long long len = w.nu - w.j < u1 - u ? w.nu - w.j : u1 - u;
+                if (w.j > 0 || w.j + len < w.nu) {
+                    // part of a tile: this CTA is one of the contributors that the ends of the tile name
+                    CHECK(w.nu > most);
+                    const int cf = run_of(u - w.j, W, P), cl = run_of(u - w.j + w.nu - 1, W, P);
+                    CHECK(cf < cl && c >= cf && c <= cl);
+                    CHECK((c == cf) == (w.j == 0) && (c == cl) == (w.j + len == w.nu));
+                    for (int x = cf; x <= cl; ++x) {
+                        WorkCur t;
+                        const long long a = run_bound(s, req, cum, B, nkv, run_start(x, W, P), most, t);
+                        const long long z = run_bound(s, req, cum, B, nkv, run_start(x + 1, W, P), most, t);
+                        CHECK(a < u - w.j + w.nu && z > u - w.j && z > a);
+                    }
+                }
+                u += len;
+                if (u < u1) next_tile(s, req, B, nkv, w);
+            }
+        }
+        CHECK(prev == W);
+    }
     printf("ok\n");
     return 0;
 }

@@ -309,6 +309,33 @@ def test_attention_sharp_scores(llb, new, seqs, dtype):
     attn_case(llb, new, seqs, 4, 2, 128, 32, dtype, seed=2, spread=16.0)
 
 
+@pytest.mark.parametrize("hd,n", [(128, 1), (64, 40)])
+def test_attention_many_small_weights(llb, hd, n):
+    """fp16, one key far above 20000 others: most of the output comes from weights near 2^-17 of the largest, below
+    fp16's normal range. They are rounded with a factor 2^7 at least, so by at most 2^-32 of the largest each."""
+    g = torch.Generator().manual_seed(14)
+    page, nkv, nh, seq, dt = 64, 1, 2, 20000, torch.float16
+    pools, tables, dense = paged_cache([seq], page, nkv, hd, dt, g)
+    k, v = dense[0]
+    k.zero_()
+    k[17] = 1.0                                       # 11.5 after the scale: weights of e^-11.5 = 2^-16.6 elsewhere
+    v.copy_(1.0 + v * 0.25)
+    for j in range(seq):
+        p, o = int(tables[0, j // page]), j % page
+        pools[0][p, 0, o] = k[j, 0]
+        pools[1][p, 0, o] = v[j, 0]
+    q = torch.full((n, nh, hd), 11.5 / hd ** 0.5).to(dt)
+    out = torch.empty(n, nh, hd, dtype=dt, device="cuda")
+    llb.paged_attention(q.cuda(), pools[0].cuda(), pools[1].cuda(), tables.cuda(), i32([0, n]), i32([seq]), out,
+                        max_new=n)
+    got = out.cpu().double()
+    for i in sorted({0, n - 1}):
+        s1 = seq - n + i + 1
+        want, tol = R.attention(q[i:i + 1], k, v, 1, s1, hd ** -0.5)
+        # against the largest weight 1, the sum is at least 1: s1 * 2^-32 more of the mean |v| < 2
+        assert ((got[i] - want[0]).abs() <= tol[0] + s1 * 2.0 ** -31).all()
+
+
 def test_attention_negative_scale(llb):
     attn_case(llb, [1, 70], [100, 200], 4, 2, 64, 16, "bf16", seed=9, scale=-0.3)
 
@@ -460,6 +487,118 @@ def test_attention_on_two_streams_and_in_graphs(llb):
             assert torch.equal(out, want) and torch.equal(e, want)
             out.zero_()
         torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("hd,nkv,max_new", [(128, 8, 1), (128, 8, 200), (64, 8, 200)])
+def test_far_pages(llb, hd, nkv, max_new):
+    """Pools of more than 2^31 values: append to and attention over their last pages."""
+    g = torch.Generator().manual_seed(19)
+    page, nh, dt = 64, 8, torch.bfloat16
+    n_pages = (1 << 31) // (nkv * page * hd) + 40
+    pools = [torch.zeros(n_pages, nkv, page, hd, dtype=dt, device="cuda") for _ in range(2)]
+    n, seq = max_new, 300
+    ids = [n_pages - 1 - 2 * i for i in range(-(-seq // page))]
+    k, v = (torch.randn(seq, nkv, hd, generator=g).to(dt) for _ in range(2))
+    pos = torch.arange(seq, dtype=torch.int32)
+    slots = torch.tensor([ids[p // page] * page + p % page for p in range(seq)])
+    rope = torch.zeros(seq, hd // 2, 2)
+    rope[..., 0] = 1.0                                # no rotation
+    st = i32([0])
+    q_out = torch.empty(seq, nh, hd, dtype=dt, device="cuda")
+    q = torch.randn(seq, nh, hd, generator=g).to(dt)
+    llb.paged_append(q.cuda(), k.cuda(), v.cuda(), pos.cuda(), slots.cuda(), rope.cuda(), q_out, *pools, status=st)
+    assert torch.equal(q_out.cpu(), q)
+    out = torch.empty(n, nh, hd, dtype=dt, device="cuda")
+    llb.paged_attention(q_out[seq - n:].contiguous(), *pools, i32([ids]), i32([0, n]), i32([seq]), out, max_new=n,
+                        status=st)
+    assert int(st) == 0
+    want, tol = R.attention(q[seq - n:], k, v, n, seq, hd ** -0.5)
+    assert ((out.cpu().double() - want).abs() <= tol).all()
+    assert int(pools[0][:n_pages - 2 * len(ids)].count_nonzero()) == 0
+    del pools
+    torch.cuda.empty_cache()
+
+
+def test_on_a_side_stream(llb):
+    """Calls on a stream given by argument and on the current one order themselves with that stream's work."""
+    g = torch.Generator().manual_seed(3)
+    page, nkv, nh, hd, dt, seq = 16, 2, 8, 128, torch.bfloat16, 500
+    pools, tables, dense = paged_cache([seq], page, nkv, hd, dt, g)
+    q = torch.randn(1, nh, hd, generator=g).to(dt)
+    want, tol = R.attention(q, *dense[0], 1, seq, hd ** -0.5)
+    dev = [x.cuda() for x in (pools[0], pools[1], tables)]
+    cu, sl = i32([0, 1]), i32([seq])
+    torch.cuda.synchronize()
+    for given in (True, False):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            late = torch.zeros(1, nh, hd, dtype=dt, device="cuda")
+            torch.cuda._sleep(20_000_000)             # the queries arrive late on s
+            late.copy_(q.cuda())
+            out = torch.empty_like(late)
+            if not given:
+                llb.paged_attention(late, *dev, cu, sl, out, max_new=1)
+        if given:
+            llb.paged_attention(late, *dev, cu, sl, out, max_new=1, stream=s)
+        s.synchronize()
+        assert ((out.cpu().double() - want).abs() <= tol).all()
+
+
+# ---------------------------------------------------------------- refusals that need tensors
+
+def test_wrong_tensors_are_refused(llb):
+    z = lambda *shape, dt=torch.bfloat16: torch.zeros(*shape, dtype=dt, device="cuda")
+    n0 = llb.launch_count()
+    q, kv, pools, rope = z(4, 8, 64), z(4, 2, 64), [z(3, 2, 16, 64) for _ in range(2)], z(9, 32, 2, dt=torch.float32)
+    pos, slots = i32([0, 1, 2, 3]), torch.arange(4, device="cuda")
+    good = [q, kv, kv, pos, slots, rope, q.clone(), *pools]
+    for i, bad in ((0, q.half()), (0, q.cpu()), (0, z(4, 8, 128)), (0, z(4, 8, 64).transpose(0, 1)), (1, z(4, 3, 64)),
+                   (2, kv.float()), (3, pos.long()), (3, pos[:3]), (4, slots.int()), (4, slots[:3]), (5, rope.half()),
+                   (5, z(9, 16, 2, dt=torch.float32)), (6, z(4, 8, 64, dt=torch.int16)), (6, z(3, 8, 64)),
+                   (7, pools[0].float()), (8, z(3, 2, 32, 64)), (7, pools[0].transpose(1, 2)), (6, z(8, 4, 64).transpose(0, 1))):
+        args = list(good)
+        args[i] = bad
+        with pytest.raises(ValueError):
+            llb.paged_append(*args)
+    with pytest.raises(ValueError):
+        llb.paged_append(*good, q_norm=z(32, dt=torch.float32))
+    with pytest.raises(ValueError):
+        llb.paged_append(*good, status=z(1, dt=torch.int64))
+    with pytest.raises(llb.LlamaError):
+        llb.paged_append(*good, eps=-1.0)
+    tab, cu, sl = i32([[0, 1]]), i32([0, 4]), i32([20])
+    ws = llb.paged_attention_workspace(q, 2, 4)
+    base = [q, *pools, tab, cu, sl, q.clone()]
+    for i, bad in ((0, q.float()), (0, z(4, 8, 32)), (1, pools[0].half()), (3, tab.long()), (3, tab[0]), (4, i32([0])),
+                   (5, i32([20, 3])), (6, z(4, 4, 64)), (6, q.cpu()), (4, cu.cpu())):
+        args = list(base)
+        args[i] = bad
+        with pytest.raises(ValueError):
+            llb.paged_attention(*args, workspace=ws)
+    with pytest.raises(llb.LlamaError):
+        llb.paged_attention(*base, workspace=ws[:1024])
+    with pytest.raises(ValueError):
+        llb.paged_attention(*base, workspace=ws.view(torch.int32))
+    with pytest.raises(llb.LlamaError):
+        llb.paged_attention(*base, workspace=ws, scale=float("nan"))
+    lg, f, out = z(3, 50, dt=torch.float32), z(3, dt=torch.float32), i32([0] * 3)
+    for args, kw in (((lg.half(), f, f, out), {}), ((lg, f[:2], f, out), {}), ((lg, f, f.double(), out), {}),
+                     ((lg, f, f, out.long()), {}), ((lg[:, ::2], f, f, out), {}), ((lg, f, f, out), dict(top_k=f)),
+                     ((lg, f, f, out), dict(top_p=f[:1])), ((lg, f, f, out), dict(min_p=f.cpu()))):
+        with pytest.raises(ValueError):
+            llb.sample_rows(*args, **kw)
+    c = i32([1, 2])
+    plan = [c, c, i32([[0, 1], [2, 3]]), i32([4, 5]), i32([2]), 16, c.clone(), i32([0] * 3), torch.zeros(4, dtype=torch.int64, device="cuda"),
+            i32([0] * 4), i32([0])]
+    for i, bad in ((1, i32([1])), (2, i32([[0, 1]])), (2, i32([0, 1])), (3, torch.zeros(2, device="cuda")), (4, i32([1, 2])),
+                   (6, c.long()), (7, i32([0] * 2)), (8, i32([0] * 4)), (9, i32([0] * 3)), (10, i32([1, 2]))):
+        args = list(plan)
+        args[i] = bad
+        with pytest.raises(ValueError):
+            llb.paged_plan(*args)
+    with pytest.raises(llb.LlamaError):
+        llb.paged_plan(*plan[:5], 17, *plan[6:])
+    assert llb.launch_count() == n0
 
 
 # ---------------------------------------------------------------- a serving run
