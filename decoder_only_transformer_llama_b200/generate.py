@@ -7,7 +7,8 @@ into a (rows, total_len) table, the first forward (llama_prefill) runs the
 first min(prompt lengths) tokens of every row, and each later position is one
 llama_decode_step of all rows at that position.  The next token comes from
 llama_sample (argmax at temperature 0, else nucleus sampling with the caller's
-uniforms); where a row's prompt still covers the position, the prompt's token
+uniforms), or from llama_sample_rows where top_k, min_p or parameters per row
+are given; where a row's prompt still covers the position, the prompt's token
 is kept instead.  A row has finished once it produced EOS outside its prompt;
 the loop ends early when every row has.  Log-probabilities come from
 llama_token_logprobs on the logits of each forward.
@@ -25,23 +26,27 @@ The driver only moves data and makes the per-step decisions the loop makes on
 the host (keep the prompt token, track EOS); every forward pass, every sampled
 token and every log-probability is computed by the library's kernels.
 """
-from typing import List, Optional, Sequence, Tuple
+from typing import List, Optional, Sequence, Tuple, Union
 
 import numpy as np
 
-from . import Model, sample, token_logprobs
+from . import Model, sample, sample_rows, token_logprobs
 
 PAD = -1
 
 
 def generate(model: Model, prompts: Sequence[Sequence[int]], max_gen_len: Optional[int] = None,
-             temperature: float = 0.6, top_p: float = 0.9, uniforms=None, logprobs: bool = False,
-             echo: bool = False, eos_id: Optional[int] = None
+             temperature: Union[float, Sequence[float]] = 0.6, top_p: Union[float, Sequence[float]] = 0.9,
+             uniforms=None, logprobs: bool = False, echo: bool = False, eos_id: Optional[int] = None,
+             top_k: Union[None, int, Sequence[int]] = None, min_p: Union[None, float, Sequence[float]] = None
              ) -> Tuple[List[List[int]], Optional[List[List[float]]]]:
     """Generate continuations of `prompts` (lists of token ids) with `model`.
 
-    uniforms: device fp32 tensor [>= total_len, len(prompts)], needed when
-    temperature > 0.  Returns (token lists, log-probability lists or None)."""
+    uniforms: device fp32 tensor [>= total_len, len(prompts)], needed when a
+    temperature is > 0.  temperature, top_p, top_k (0: off) and min_p (0: off)
+    are one value or one per prompt; with top_k, min_p or any list each step
+    samples with llama_sample_rows.  Returns (token lists, log-probability
+    lists or None)."""
     import torch
 
     a = model.args
@@ -56,7 +61,21 @@ def generate(model: Model, prompts: Sequence[Sequence[int]], max_gen_len: Option
     if max_gen_len is None:
         max_gen_len = S - 1
     total = min(S, max_gen_len + max(lens))
-    if temperature > 0 and (uniforms is None or uniforms.shape[0] < total or uniforms.shape[1] != B):
+
+    def per_row(value, off, name):
+        rows = [off if value is None else value] * B if value is None or np.isscalar(value) else list(value)
+        if len(rows) != B:
+            raise ValueError(f"{name} has {len(rows)} entries for {B} prompts")
+        return rows
+
+    by_row = top_k is not None or min_p is not None or not (np.isscalar(temperature) and np.isscalar(top_p))
+    temps = per_row(temperature, 0.0, "temperature")
+    if by_row:
+        params = [torch.tensor(v, dtype=t, device=dev) for v, t in
+                  ((temps, torch.float32), (per_row(top_k, 0, "top_k"), torch.int32),
+                   (per_row(top_p, 1.0, "top_p"), torch.float32), (per_row(min_p, 0.0, "min_p"), torch.float32))]
+        greedy_u = torch.zeros(B, dtype=torch.float32, device=dev)
+    if max(temps) > 0 and (uniforms is None or uniforms.shape[0] < total or uniforms.shape[1] != B):
         raise ValueError(f"sampling needs uniforms of shape [>= {total}, {B}]")
 
     tok = np.full((B, total), PAD, dtype=np.int64)
@@ -100,11 +119,16 @@ def generate(model: Model, prompts: Sequence[Sequence[int]], max_gen_len: Option
             pos.fill_(prev)
             model.decode_step(x, pos, logits=last_lg)
             rows = last_lg
-        if temperature > 0:
+        if by_row:
+            sample_rows(last_lg, params[0], greedy_u if uniforms is None else uniforms[cur].contiguous(), nxt,
+                        top_k=params[1], top_p=params[2], min_p=params[3])
+        elif temperature > 0:
             sample(last_lg, temperature, top_p, uniforms[cur].contiguous(), nxt)
         else:
             sample(last_lg, 0.0, top_p, None, nxt)
         chosen = nxt.cpu().numpy().astype(np.int64)
+        if chosen.min() < 0:
+            raise ValueError(f"sampling parameters of prompt {int(chosen.argmin())} are out of range")
         tok[:, cur] = np.where(in_prompt[:, cur], tok[:, cur], chosen)
         if logprobs:
             logprobs_of(rows, prev + 1, cur + 1)
