@@ -381,6 +381,10 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
             }
             warp_commit(&s_full[t]);
         };
+        // what an early look at a barrier left open
+        auto settle = [&](bool seen, uint64_t* bar, uint32_t parity) {
+            return __all_sync(0xffffffffu, seen) || warp_wait(bar, parity);
+        };
         do {
             const int nt = two_halves(sg) ? 2 : 1;
             ok = warp_wait(&q_full, nseg & 1) && warp_wait(&kv_full[slot], full_phase);
@@ -390,33 +394,42 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
             warp_commit(&kv_empty[slot]);
             if (sg.len == 1) warp_commit(&q_empty);
             advance();
-            for (int i = 0; ok && i < sg.len; ++i) {
-                ok = warp_wait(&kv_full[slot], full_phase);          // V of this unit
-                if (!ok) break;
-                const int vslot = slot;
-                advance();
-                const int kslot = slot;                              // K of the next one
+            for (int i = 0; i < sg.len; ++i) {
+                // Barriers are asked ahead of the MMAs they gate, while earlier ones
+                // run: a wait costs about 130 cycles even if it need not wait.
                 const bool more = i + 1 < sg.len;
+                const int vslot = slot;
+                const uint32_t v_phase = full_phase;
+                advance();
+                const int kslot = slot;                              // K of the next unit
+                bool v_ready = mbar_try_wait(&kv_full[vslot], v_phase);
+                bool ready = mbar_try_wait(&p_full[0][0], p_phase[0]);
+                bool k_ready = !more || mbar_try_wait(&kv_full[kslot], full_phase);
+                ok = settle(v_ready, &kv_full[vslot], v_phase);
+                const uint64_t vd = v_desc + static_cast<uint32_t>(vslot * (TILE >> 4));
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    if (t >= nt || !ok) break;
-                    const uint64_t vd = v_desc + static_cast<uint32_t>(vslot * (TILE >> 4));
+                    if (t >= nt) break;
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {                    // 64 keys at a time
-                        ok = warp_wait(&p_full[t][h], p_phase[t]);
+                        ok = ok && settle(ready, &p_full[t][h], p_phase[t]);
                         if (!ok) break;
                         tc_fence_after();
+                        // the next P half: of this sub-tile, or of the other one
+                        if (h == 0) ready = mbar_try_wait(&p_full[t][1], p_phase[t]);
+                        else if (t == 0 && nt == 2) ready = mbar_try_wait(&p_full[1][0], p_phase[1]);
 #pragma unroll
                         for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
                             warp_mma_ts(tmem + kColO + 128 * t, tmem + kColS + 128 * t + 8 * kk,
-                                         vd + (kk * 16 * 128 >> 4), idesc_o, i > 0 || kk > 0);
+                                        vd + (kk * 16 * 128 >> 4), idesc_o, i > 0 || kk > 0);
                     }
                     if (!ok) break;
                     p_phase[t] ^= 1;
                     warp_commit(&o_full[t]);
                     if (more) {
-                        if (t == 0) ok = warp_wait(&kv_full[kslot], full_phase);
+                        if (t == 0) ok = settle(k_ready, &kv_full[kslot], full_phase);
                         if (!ok) break;
+                        if (t == 0) tc_fence_after();
                         scores(t, kslot);
                     }
                 }
