@@ -40,8 +40,8 @@ namespace llb {
 namespace {
 constexpr int kThreads = 384;                // three warpgroups; warps 10 and 11 only fill the third
 // registers a thread: the launch's 168, of which the third warpgroup gives up
-// what the two softmax warpgroups take (2 * 216 + 72 = 3 * 168)
-constexpr int kRegsSoftmax = 216, kRegsOther = 72;
+// what the two softmax warpgroups take (2 * 208 + 88 = 3 * 168; 216 + 72 spills in the MMA warp, 1% slower)
+constexpr int kRegsSoftmax = 208, kRegsOther = 88;
 constexpr int kRows = 256;
 constexpr int kKeys = 128;
 constexpr int kBox = 128 * 128;             // 128 rows of 64 16-bit values
