@@ -14,9 +14,9 @@
 // serves all of its heads.  What a thread does besides its heads costs about as
 // much as one of them: three heads a thread where a token has enough, one where
 // a CTA takes a token in one go or the step is short (16384 tokens of 48 heads,
-// 16-bit, with norms: 85 us with three, 122 with one and 105 with two in CTAs of
-// 256, which leave a quarter of the places empty; 64 tokens of 80 heads: 2.5 us
-// with one, 2.9 with three).
+// 16-bit, with norms: 81 us with three, 5.05 TB/s; 122 with one and 105 with two in
+// CTAs of 256, which leave a quarter of the places empty; 64 tokens of 80 heads:
+// 2.5 us with one, 2.9 with three).
 #include <type_traits>
 
 #include "common.cuh"
@@ -87,47 +87,38 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
         if (threadIdx.x == 0) report_status(a.status, LLAMA_ERR_CAPACITY);
         return;
     }
-    float cs[N], sn[N];                                    // of both vectors' pairs
+    // Both vectors' rotations at once where they take few registers (fp32 input),
+    // else one after the other (16-bit: 64 registers instead of 87, 86 -> 81 us for
+    // 16384 tokens of 48 heads).
+    constexpr bool kBoth = sizeof(TI) == 4;
+    float4 turn[kBoth ? 2 : 1][N / 4];
+    const float4* turns = reinterpret_cast<const float4*>(a.rope + static_cast<long long>(pos) * (HD / 2) + sub * (N / 2));
 #pragma unroll
-    for (int v = 0; v < 2; ++v) {
-        const float4* r = reinterpret_cast<const float4*>(a.rope + static_cast<long long>(pos) * (HD / 2) + v * (HD / 4) + sub * (N / 2));
+    for (int v = 0; v < (kBoth ? 2 : 1); ++v)
 #pragma unroll
-        for (int i = 0; i < N / 4; ++i) {
-            const float4 f = __ldg(r + i);
-            cs[v * (N / 2) + 2 * i] = f.x; sn[v * (N / 2) + 2 * i] = f.y;
-            cs[v * (N / 2) + 2 * i + 1] = f.z; sn[v * (N / 2) + 2 * i + 1] = f.w;
-        }
-    }
+        for (int i = 0; i < N / 4; ++i) turn[v][i] = __ldg(turns + v * (HD / 8) + i);
     // a position's rows of one page's heads lie 2^page_shift rows apart
     const long long cell = (((slot >> a.page_shift) * a.nkv) << a.page_shift) + (slot & ((1LL << a.page_shift) - 1));
-    const bool norms = a.q_norm || a.k_norm;
+    float inv[kHeads];                                     // 1 / rms of each head
+    if (a.q_norm || a.k_norm) {                            // the same for every thread: the shuffles stay warp-wide
 #pragma unroll
-    for (int e = 0; e < kHeads; ++e) {
-        const int h = h0 + e * GROUPS;
-        const bool live = h < heads, is_q = h < a.nh, is_k = !is_q && h < a.nh + a.nkv;
-        float x[2][N];
-        unpack<TI, N>(raw[e][0], x[0]);
-        unpack<TI, N>(raw[e][1], x[1]);
-        if (norms) {                                       // the same for every thread: the shuffles stay warp-wide
-            float s0 = 0.f, s1 = 0.f;
+        for (int e = 0; e < kHeads; ++e) {
+            float x[2][N], s0 = 0.f, s1 = 0.f;
+            unpack<TI, N>(raw[e][0], x[0]);
+            unpack<TI, N>(raw[e][1], x[1]);
 #pragma unroll
             for (int i = 0; i < N; ++i) { s0 = fmaf(x[0][i], x[0][i], s0); s1 = fmaf(x[1][i], x[1][i], s1); }
             s0 += s1;
 #pragma unroll
             for (int o = LPH / 2; o > 0; o >>= 1) s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-            const float* w = is_q ? a.q_norm : is_k ? a.k_norm : nullptr;
-            if (w) {
-                const float inv = rsqrtf(s0 * (1.f / HD) + a.eps);
-#pragma unroll
-                for (int v = 0; v < 2; ++v)
-#pragma unroll
-                    for (int i = 0; i < N; i += 4) {
-                        const float4 f = __ldg(reinterpret_cast<const float4*>(w + v * (HD / 2) + sub * N + i));
-                        x[v][i] *= inv * f.x; x[v][i + 1] *= inv * f.y; x[v][i + 2] *= inv * f.z; x[v][i + 3] *= inv * f.w;
-                    }
-            }
+            inv[e] = rsqrtf(s0 * (1.f / HD) + a.eps);
         }
-        if (!live) continue;
+    }
+    // vector v of head e, rotated by f
+    auto finish = [&](int e, int v, const float4 (&f)[N / 4]) {
+        const int h = h0 + e * GROUPS;
+        const bool is_q = h < a.nh, is_k = !is_q && h < a.nh + a.nkv;
+        if (h >= heads) return;
         TO* dst;
         if (is_q) {
             dst = static_cast<TO*>(a.q_out) + (static_cast<long long>(t) * a.nh + h) * HD;
@@ -135,24 +126,44 @@ __global__ void __launch_bounds__(kThreads) paged_append_kernel(AppendArgs a) {
             const int g = is_k ? h - a.nh : h - a.nh - a.nkv;
             dst = static_cast<TO*>(is_k ? a.k_pages : a.v_pages) + (cell + (static_cast<long long>(g) << a.page_shift)) * HD;
         }
-        dst += sub * N;
+        dst += sub * N + v * (HD / 2);
+        float x[N];
+        unpack<TI, N>(raw[e][v], x);
+        if (is_q || is_k) {
+            const float* w = is_q ? a.q_norm : a.k_norm;
+            if (w) {
 #pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            if (is_q || is_k) {
-                float y[N];
-#pragma unroll
-                for (int i = 0; i < N / 2; ++i) {
-                    const float c = cs[v * (N / 2) + i], n = sn[v * (N / 2) + i];
-                    y[2 * i] = x[v][2 * i] * c - x[v][2 * i + 1] * n;
-                    y[2 * i + 1] = x[v][2 * i] * n + x[v][2 * i + 1] * c;
+                for (int i = 0; i < N; i += 4) {
+                    const float4 g = __ldg(reinterpret_cast<const float4*>(w + v * (HD / 2) + sub * N + i));
+                    x[i] *= inv[e] * g.x; x[i + 1] *= inv[e] * g.y; x[i + 2] *= inv[e] * g.z; x[i + 3] *= inv[e] * g.w;
                 }
-                store_vec<TO, N>(dst + v * (HD / 2), y);
-            } else if constexpr (std::is_same<TI, TO>::value) {
-                *reinterpret_cast<uint4*>(dst + v * (HD / 2)) = raw[e][v];     // the value's own bits
-            } else {
-                store_vec<TO, N>(dst + v * (HD / 2), x[v]);
             }
+            float y[N];
+#pragma unroll
+            for (int i = 0; i < N / 4; ++i) {              // two pairs: (cos, sin), (cos, sin)
+                const float* p = x + 4 * i;
+                y[4 * i] = p[0] * f[i].x - p[1] * f[i].y;
+                y[4 * i + 1] = p[0] * f[i].y + p[1] * f[i].x;
+                y[4 * i + 2] = p[2] * f[i].z - p[3] * f[i].w;
+                y[4 * i + 3] = p[2] * f[i].w + p[3] * f[i].z;
+            }
+            store_vec<TO, N>(dst, y);
+        } else if constexpr (std::is_same<TI, TO>::value) {
+            *reinterpret_cast<uint4*>(dst) = raw[e][v];                        // the value's own bits
+        } else {
+            store_vec<TO, N>(dst, x);
         }
+    };
+    if constexpr (kBoth) {
+#pragma unroll
+        for (int e = 0; e < kHeads; ++e) { finish(e, 0, turn[0]); finish(e, 1, turn[1]); }
+    } else {
+#pragma unroll
+        for (int e = 0; e < kHeads; ++e) finish(e, 0, turn[0]);
+#pragma unroll
+        for (int i = 0; i < N / 4; ++i) turn[0][i] = __ldg(turns + HD / 8 + i);
+#pragma unroll
+        for (int e = 0; e < kHeads; ++e) finish(e, 1, turn[0]);
     }
 }
 
