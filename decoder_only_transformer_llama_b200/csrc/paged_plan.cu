@@ -21,6 +21,7 @@ constexpr int kThreads = 512;
 constexpr int kPer = kPagedMaxRequests / kThreads;   // requests per thread
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCtas = 8;
+constexpr long long kMaxTokens = 1LL << 30;          // of one request, as in paged attention
 
 // The last of n ascending entries that is <= v (a[0] <= v).
 __device__ __forceinline__ int last_le(const int* a, int n, int v) {
@@ -61,7 +62,7 @@ __global__ void __launch_bounds__(kThreads) paged_plan_kernel(PlanArgs a, int sh
         v[1] += ended[e] ? have[e] : 0;
         v[2] += want[e];
         if (ctx[e] < 0) err = LLAMA_ERR_INVALID_ARG;
-        else if (!err && have[e] + want[e] > a.max_pages) err = LLAMA_ERR_CAPACITY;
+        else if (!err && (have[e] + want[e] > a.max_pages || ctx[e] + n[e] > kMaxTokens)) err = LLAMA_ERR_CAPACITY;
     }
     long long incl[3] = {v[0], v[1], v[2]};
 #pragma unroll

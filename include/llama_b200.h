@@ -219,8 +219,8 @@ LLAMA_API int llama_sample(const float* logits, int B, int V, float temperature,
  * largest logit is +inf, the tokens at +inf share the mass equally.  A row
  * without any logit above -inf gives token 0.  A row whose temperature is
  * negative, NaN or infinite, whose top_p is negative or NaN, or whose min_p
- * is outside [0, 1] or NaN gives -1.  With top_k and min_p off and V tokens
- * of distinct mass the picks are those of llama_sample.  Needs no model and
+ * is outside [0, 1] or NaN gives -1.  With top_k and min_p off the picks on
+ * finite logits are those of llama_sample.  Needs no model and
  * no workspace.  LLAMA_ERR_INVALID_ARG for NULL pointers and sizes out of
  * range; B == 0 is a no-op. */
 LLAMA_API int llama_sample_rows(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,

@@ -104,7 +104,8 @@ LLAMA_API int llama_op_linear_noalloc(const void* A, const void* W, int M, int N
  *               behind the last row.  T is the arrays' length, at least the step's total
  *   free_left   int32 [1] out: free pages after the step (may be free_count itself)
  * All or nothing: if the step needs more pages than are free, more than
- * max_pages per request or more than T rows (LLAMA_ERR_CAPACITY in status), or a
+ * max_pages (or 2^30 tokens) per request or more than T rows (LLAMA_ERR_CAPACITY in
+ * status), or a
  * ctx or free_count is negative or more pages are free than n_pages
  * (LLAMA_ERR_INVALID_ARG), nothing is taken or returned: every request adds no
  * token (cu_new all 0, slots and positions -1) and seq_lens and free_left repeat
@@ -149,7 +150,9 @@ LLAMA_API int llama_paged_append(const void* q, int64_t q_stride, const void* k,
  *   workspace   llama_paged_attention_workspace_bytes() of device scratch,
  *               256-byte aligned, zero-filled before its first use (the kernels
  *               leave their counters at zero); calls sharing one must not
- *               overlap on the device.  A workspace for one max_new serves smaller ones.
+ *               overlap on the device.  A workspace for one max_new serves smaller
+ *               ones.  Zero it again after LLAMA_ERR_DEVICE_TIMEOUT in status (a
+ *               bounded wait of the chunk kernel gave up; outputs unspecified).
  * A row that sees no key (seq_lens[b] < n) gives zeros; rows behind the last
  * request are left as they were.  Keys behind a request's last token and keys
  * a row may not see do not reach its output, whatever their slots hold (NaN

@@ -89,6 +89,7 @@ def test_plan(llb, case, alias):
     ([10, -1], [7, 1], 16, 5, 3, 64, None, 1),
     ([64, 64], [-1, -1], 16, 2, 4, 4, 9, 1),             # ten free pages in a list of nine
     ([2147483000], [1000], 16, 5, 3, 64, None, 2),       # past the positions of an int
+    ([3, -5, 70], [80, 1, 9], 16, 1, 6, 4, None, 1),     # several faults: a bad argument goes first
 ])
 def test_plan_all_or_nothing(llb, ctx, new, page, extra, width, room, cap, code):
     real = [c if c < 1 << 20 else 0 for c in ctx]
@@ -293,6 +294,14 @@ ATTN = [
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 def test_attention(llb, case, dtype):
     attn_case(llb, *ATTN[case], dtype, seed=case)
+
+
+@pytest.mark.parametrize("dtype,hd,max_new", [("bf16", 128, 1), ("f16", 128, 300), ("bf16", 64, 300), ("f32", 32, 1)])
+def test_attention_a_thousand_requests(llb, dtype, hd, max_new):
+    """As many requests as a call may hold, a third of them without new tokens, some with a few."""
+    new = [(0, 1, 1, 0, 1, 3)[b % 6] for b in range(1024)]
+    seqs = [new[b] + (b * 7) % 40 for b in range(1024)]
+    attn_case(llb, new, seqs, 2, 1, hd, 16, dtype, seed=1, max_new=max_new)
 
 
 @pytest.mark.parametrize("max_new", [1, 300])
