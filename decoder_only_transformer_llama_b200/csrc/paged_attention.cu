@@ -13,6 +13,12 @@
 // request's last key and pages outside the pool read as zeros) in a ring of
 // three.
 //
+// Measured: 32 tokens over 1000-2000 keys (32 heads of 128, bf16, pages of 16) 133 us,
+// 5.8 TB/s; one token over 53000 keys (64/8 heads, fp16) 46 us, 6.0 TB/s in its loop,
+// 6 us before it and 6 behind it; 190 keys 7.7 us.  32 KB units three deep with two
+// CTAs per SM keep 128 KB in flight on each; TMA boxes would need a map per page
+// size and could not zero the rows behind the last key.
+//
 // 16-bit caches: warp w takes keys 16 w .. 16 w + 15 of a unit for all 16 rows,
 // S = Q K^T and O += P V as mma.sync m16n8k16 fragments (a tile of 16 rows is
 // far below tcgen05's 128; longer chunks take the kernel of

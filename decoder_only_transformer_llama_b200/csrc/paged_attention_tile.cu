@@ -19,6 +19,13 @@
 // unit may overwrite P_t once its product is issued.  m moves only when a unit
 // raises it by more than 8 (a factor 256): then O_t is rescaled in TMEM.
 //
+// Measured: chunks of 1000-2000 tokens over 3000-6000 keys (64/8 heads of 128, bf16)
+// 486 us, 1158 TFLOP/s; 560 us under the power cap.  A unit takes about 4000 cycles, of
+// which the MMAs are 2048: bound by the chain scores -> softmax -> product of a
+// sub-tile, which the other one covers only in part (TMEM has no room for a third).
+// 256 rows a tile so that K and V tiles are read once for both sub-tiles; 128 keys a
+// unit so that S_t and O_t fill TMEM.
+//
 // K and V tiles come by TMA, one box per page (64 columns x min(page, 128)
 // rows); pages behind the keys or outside the pool are read at a coordinate
 // behind the pool, which fills zeros.

@@ -9,8 +9,10 @@
 // the ended request that returns it above.  So each CTA scans the lengths by
 // itself and writes its share of slots, pages and offsets from the inputs
 // alone; a cluster barrier between the last read of an input and the first
-// write lets seq_lens and free_left be the inputs they follow.  Latency bound:
-// a step moves a few hundred kilobytes at most.
+// write lets seq_lens and free_left be the inputs they follow.  Latency bound (a
+// step moves a few hundred kilobytes at most): 3.5 us for 32 decodes, 7.9 us for
+// 256 requests with 11000 new tokens; one CTA with a thread per request that
+// moved its pages one after the other took 23.6 us for the former.
 #include "common.cuh"
 #include "paged.h"
 

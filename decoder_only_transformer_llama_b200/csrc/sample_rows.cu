@@ -14,6 +14,11 @@
 // 64-bit fixed point (2^-46 resolution): every prefix sum is an exact integer
 // in any order, and tokens below 2^-47 of the maximum weigh nothing.
 //
+// Measured: 1 x 32000 logits 11 us (six exchanges over the cluster, latency), 64 x 128000
+// with parameters of every kind 73 us (issue-bound: some 90 instructions per logit of a row
+// without top-k; rows with top-k 36 us), against 1.28 ms and 5.2 ms of one CTA per row
+// with a radix select over whole-row passes.
+//
 // A row is spread over a cluster of R = 8, 4 or 2 CTAs.  A histogram over 1024 equal steps
 // of l_max - l (bins are ordered like the tokens), summed over the cluster
 // through distributed shared memory, turns each of the three searches (k-th
@@ -643,7 +648,8 @@ static int rows_keep(const float* logits, int B, int V, const float* temperature
 
 int launch_sample_rows(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
                        const float* top_p, const float* min_p, const float* uniforms, int32_t* out, cudaStream_t st) {
-    // the widest clusters whose rows all fit on the GPU at once (two CTAs an SM)
+    // the widest clusters whose rows all fit on the GPU at once (two CTAs an SM): 64 rows of
+    // 128000 with top-k 36 us on clusters of 4, 49 on 8; 32 rows 26 us on 8
     if (B <= 32) return rows_keep<8>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
     if (B <= 64) return rows_keep<4>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
     return rows_keep<2>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
