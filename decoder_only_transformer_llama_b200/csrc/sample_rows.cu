@@ -63,7 +63,7 @@ struct RowShared {
     int seg_n[2];
     u64 red_a[kWarps], red_b[kWarps];
     float red_f[kWarps], red_g[kWarps];
-    double table[64];                         // 2^(-j / 64)
+    double table[128];                        // 2^(-j / 128)
     int bin, hit;
 };
 
@@ -95,61 +95,61 @@ __device__ __forceinline__ void st_peer32(const void* p, uint32_t rank, unsigned
     asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(cluster_addr(p, rank)), "r"(v) : "memory");
 }
 
-// One row's scales.  e = 2^(-y / 64), y = (l_max - l) * c64 with c64 = 64 log2(e) / T.
+// One row's scales.  e = 2^(-y / 128), y = (l_max - l) * c128 with c128 = 128 log2(e) / T.
 struct Scale {
     float lmax, reach;   // distances beyond `reach` weigh nothing
-    double dmax, c64;    // l_max (0 if infinite)
+    double dmax, c128;   // l_max
     float cbin;          // bins per unit of l_max - l
 };
 
-// Tokens that may weigh something (the equals of an infinite maximum too; never NaN or -inf).
-__device__ __forceinline__ bool within(const Scale& s, float l) { return l == s.lmax || s.lmax - l <= s.reach; }
+// Tokens that may weigh something (never NaN or -inf).
+__device__ __forceinline__ bool within(const Scale& s, float l) { return s.lmax - l <= s.reach; }
 
-// e * 2^46 at y >= 0 below 68000: y = n + r, |r| <= 1/2, is cut into n = 64 q + j, and
-// 2^(-y/64) = 2^-q * 2^(-j/64) * exp(-r ln2 / 64) with the exponential's Taylor
-// terms up to the fifth power (|r ln2 / 64| < 0.0055: the rest is below 4e-17).
-// Table-driven exponentials after Tang (1989).
+// e * 2^46 at 0 <= y < 2^13 (anything elsewhere): y = n - r, |r| <= 1/2, is cut into n =
+// 128 q + j, and 2^(-y/128) = 2^-q * 2^(-j/128) * exp(r ln2 / 128) with the exponential's
+// Taylor terms up to the fourth power (|r ln2 / 128| < 0.0028: the rest is below
+// 1.3e-15, a tenth of the masses' resolution).  Table-driven exponentials after Tang (1989).
 __device__ __forceinline__ double scaled_exp(const RowShared& sh, double y) {
     constexpr double kMagic = 6755399441055744.0;              // 1.5 * 2^52: adding it rounds to an integer
+    constexpr double c = 0.69314718055994530942 / 128.0;
     const double t = y + kMagic;
-    const int n = static_cast<int>(__double_as_longlong(t) & 0xffffffffLL);
-    const double z = (t - kMagic - y) * (0.69314718055994530942 / 64.0);
-    double p = fma(z, 1.0 / 120.0, 1.0 / 24.0);
-    p = fma(p, z, 1.0 / 6.0);
-    p = fma(p, z, 0.5);
-    p = fma(p, z, 1.0);
-    p = fma(p, z, 1.0);
-    const double s = __longlong_as_double(static_cast<long long>(1023 + 46 - (n >> 6)) << 52);
-    return sh.table[n & 63] * p * s;
+    const int n = __double2loint(t);
+    const double r = (t - kMagic) - y;
+    double p = fma(r, c * c * c * c / 24.0, c * c * c / 6.0);
+    p = fma(p, r, c * c / 2.0);
+    p = fma(p, r, c);
+    p = fma(p, r, 1.0);
+    p *= sh.table[n & 127];
+    return __hiloint2double(__double2hiint(p) + (46 << 20) - ((n & ~127) << 13), __double2loint(p));   // * 2^(46 - q)
 }
 // The mass of a logit (0 out of reach), and whether min-p keeps it (e >= mp).
 // Without branches: four of them overlap.
 __device__ __forceinline__ u64 row_mass(const RowShared& sh, const Scale& s, float l, double mp46, bool* keep) {
     const bool in = within(s, l);
-    const double d = in && l != s.lmax ? s.dmax - static_cast<double>(l) : 0.0;
-    const double e = scaled_exp(sh, d * s.c64);
-    *keep = e >= mp46;
-    const u64 m = static_cast<u64>(__double_as_longlong(e + 4503599627370496.0) & 0xfffffffffffffLL);   // + 2^52: rounds
-    return in ? m : 0ull;
+    const double e = scaled_exp(sh, (s.dmax - static_cast<double>(l)) * s.c128);
+    *keep = in && e >= mp46;
+    const double m = e + 4503599627370496.0;                   // + 2^52: rounds to an integer in the low bits
+    const uint32_t lo = in ? __double2loint(m) : 0u, hi = in ? __double2hiint(m) & 0xfffff : 0u;
+    return (static_cast<u64>(hi) << 32) | lo;
 }
 __device__ __forceinline__ int row_bin(const Scale& s, float l) {
-    const float y = l == s.lmax ? 0.f : (s.lmax - l) * s.cbin;
-    return min(static_cast<int>(y), kBins - 1);
+    return min(static_cast<int>((s.lmax - l) * s.cbin), kBins - 1);
 }
 
 // The step within its bin, of 1024 (the bin number takes at most 10 bits of the
 // product's 24, so the steps are ordered like the tokens too).
 __device__ __forceinline__ int row_step(const Scale& s, float l) {
-    const float y = l == s.lmax ? 0.f : (s.lmax - l) * s.cbin;
+    const float y = (s.lmax - l) * s.cbin;
     return min(static_cast<int>((y - static_cast<float>(min(static_cast<int>(y), kBins - 1))) * kBins), kBins - 1);
 }
 
 // Adds a token to this CTA's histogram.
 __device__ __forceinline__ void hist_add(RowShared& sh, int bin, u64 m) {
+    const uint32_t lo = static_cast<uint32_t>(m), hi = static_cast<uint32_t>(m >> 32);
     atomicAdd(&sh.h[0][bin], 1u);
-    atomicAdd(&sh.h[1][bin], static_cast<unsigned int>(m & 0xffffu));
-    atomicAdd(&sh.h[2][bin], static_cast<unsigned int>((m >> 16) & 0xffffu));
-    atomicAdd(&sh.h[3][bin], static_cast<unsigned int>(m >> 32));
+    atomicAdd(&sh.h[1][bin], lo & 0xffffu);
+    atomicAdd(&sh.h[2][bin], lo >> 16);
+    atomicAdd(&sh.h[3][bin], hi);
 }
 __device__ __forceinline__ void hist_clear(RowShared& sh) {
     for (int i = threadIdx.x; i < 4 * kBins; i += kThreads) sh.h[i / kBins][i % kBins] = 0u;
@@ -238,7 +238,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     const int k = top_k ? top_k[b] : 0;
     const float tp = top_p ? top_p[b] : 1.f;
     const float mp = min_p ? min_p[b] : 0.f;
-    if (!(T >= 0.f) || T == INFINITY || !(tp >= 0.f) || !(mp >= 0.f) || mp > 1.f) {
+    if (!(T >= 0.f) || T > 1e30f || !(tp >= 0.f) || !(mp >= 0.f) || mp > 1.f) {
         if (rank == 0 && threadIdx.x == 0) out[b] = -1;
         return;                                // the whole cluster, before any exchange
     }
@@ -262,6 +262,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         v.w = j + 3 < n ? __ldg(row + j + 3) : -INFINITY;
         return v;
     };
+    bool infinite = false;
     // f(four logits, first id) for every vector of the slice (-inf outside it)
     auto each4 = [&](auto f) __attribute__((always_inline)) {
         for (int i0 = threadIdx.x; i0 < nv; i0 += kBatch * kThreads) {
@@ -275,7 +276,11 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
             for (int x = 0; x < kBatch; ++x) {
                 const int i = i0 + x * kThreads;
                 if (i >= nv) break;
-                const float l[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+                float l[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
+                if (infinite) {                // only the equals of an infinite maximum weigh anything
+#pragma unroll
+                    for (int y = 0; y < 4; ++y) l[y] = l[y] == INFINITY ? 0.f : -INFINITY;
+                }
                 f(l, lo + 4 * i - mis);
             }
         }
@@ -294,7 +299,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         });
     };
     // ---- the largest logit of the row and its smallest finite one
-    if (threadIdx.x < 64) sh.table[threadIdx.x] = exp2(-static_cast<double>(threadIdx.x) / 64.0);
+    if (threadIdx.x < 128) sh.table[threadIdx.x] = exp2(-static_cast<double>(threadIdx.x) / 128.0);
     hist_clear(sh);
     if (threadIdx.x == 0) { sh.hit = 0; sh.bin = 0; }
     float lmax = -INFINITY, least = INFINITY;
@@ -328,6 +333,8 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     cluster_sync();
     lmax = warp_max(lane < R ? __uint_as_float(ld_peer32(&sh.x_max, lane)) : -INFINITY);
     least = -warp_max(lane < R ? -__uint_as_float(ld_peer32(&sh.x_min, lane)) : -INFINITY);
+    infinite = lmax == INFINITY;
+    if (infinite) lmax = least = 0.f;
     if (T == 0.f || lmax == -INFINITY) {
         // greedy: the lowest id at the maximum (a row without a finite logit: token 0)
         int id0 = 0x7fffffff;
@@ -351,14 +358,13 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     }
     Scale sc;
     sc.lmax = lmax;
-    sc.c64 = 64.0 * 1.4426950408889634074 / static_cast<double>(T);
+    sc.c128 = 128.0 * 1.4426950408889634074 / static_cast<double>(T);
     // distances beyond `reach` weigh nothing; without top-k and top-p, neither
     // do those that min-p drops (a little further, for its own exact test)
     float reach = fminf(kReach * T, lmax - least);
     if (k <= 0 && tp >= 1.f && mp > 0.f) reach = fminf(reach, (-logf(mp) * 1.0001f + 1e-4f) * T);
-    if (lmax == INFINITY) reach = 0.f;         // only its equals weigh anything
     sc.reach = reach;
-    sc.dmax = lmax == INFINITY ? 0.0 : static_cast<double>(lmax);
+    sc.dmax = static_cast<double>(lmax);
     sc.cbin = reach > 0.f ? static_cast<float>(kBins) / reach : 0.f;
     if (!(sc.cbin < INFINITY)) sc.cbin = 3e38f;
     const double mp46 = static_cast<double>(mp) * kFix;
@@ -479,14 +485,14 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     // ---- histogram of masses; the row's mass and min-p's
     u64 zm = 0;
     each4([&](const float (&l)[4], int) {
-        if (!within(sc, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])))) return;
+        if (!within(sc, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])))) return;   // all four weigh nothing
         u64 m[4];
         int at[4];
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
             bool keep;
             m[y] = row_mass(sh, sc, l[y], mp46, &keep);
-            zm += keep ? m[y] : 0ull;
+            if (mp > 0.f && keep) zm += m[y];
             at[y] = row_bin(sc, l[y]);
         }
 #pragma unroll
@@ -604,7 +610,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
             z = zp < z ? zp : z;
         }
     }
-    z = zm < z ? zm : z;
+    if (mp > 0.f && zm < z) z = zm;
     __syncthreads();
     finish(find(false, static_cast<u64>(u * static_cast<double>(z))));
 }

@@ -218,7 +218,7 @@ LLAMA_API int llama_sample(const float* logits, int B, int V, float temperature,
  * A NaN logit counts as -inf and a token at -inf is never drawn; if the
  * largest logit is +inf, the tokens at +inf share the mass equally.  A row
  * without any logit above -inf gives token 0.  A row whose temperature is
- * negative, NaN or infinite, whose top_p is negative or NaN, or whose min_p
+ * negative, NaN or above 1e30, whose top_p is negative or NaN, or whose min_p
  * is outside [0, 1] or NaN gives -1.  With top_k and min_p off the picks on
  * finite logits are those of llama_sample.  Needs no model and
  * no workspace.  LLAMA_ERR_INVALID_ARG for NULL pointers and sizes out of

@@ -111,7 +111,7 @@ def sample(logits, temperature, top_k, top_p, min_p, u):
     V = logits.numel()
     l = logits.double().clone()
     l[l.isnan()] = -math.inf
-    if not (0 <= temperature < math.inf) or not top_p >= 0 or not 0 <= min_p <= 1:
+    if not 0 <= temperature <= 1e30 or not top_p >= 0 or not 0 <= min_p <= 1:
         return -1
     order = torch.sort(l, descending=True, stable=True).indices
     top = l[order[0]]
