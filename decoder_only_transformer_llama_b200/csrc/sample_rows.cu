@@ -15,8 +15,8 @@
 // in any order, and tokens below 2^-47 of the maximum weigh nothing.
 //
 // Measured: 1 x 32000 logits 11 us (six exchanges over the cluster, latency), 64 x 128000
-// with parameters of every kind 73 us (issue-bound: some 90 instructions per logit of a row
-// without top-k; rows with top-k 36 us), against 1.28 ms and 5.2 ms of one CTA per row
+// with parameters of every kind 66 us (issue-bound: some 70 instructions per logit of a row
+// without top-k; rows with top-k 33 us), against 1.28 ms and 5.2 ms of one CTA per row
 // with a radix select over whole-row passes.
 //
 // A row is spread over a cluster of R = 8, 4 or 2 CTAs.  A histogram over 1024 equal steps
@@ -132,15 +132,19 @@ __device__ __forceinline__ u64 row_mass(const RowShared& sh, const Scale& s, flo
     const uint32_t lo = in ? __double2loint(m) : 0u, hi = in ? __double2hiint(m) & 0xfffff : 0u;
     return (static_cast<u64>(hi) << 32) | lo;
 }
-__device__ __forceinline__ int row_bin(const Scale& s, float l) {
-    return min(static_cast<int>((s.lmax - l) * s.cbin), kBins - 1);
+// A token's bin, the distance in steps rounded to an integer: as a float, 2^23 + bin
+// (ordered like the tokens; two additions and no conversion), and as a number.
+constexpr float kBinBase = 8388608.f;
+__device__ __forceinline__ float row_place(const Scale& s, float l) {
+    return fminf(fmaf(s.lmax - l, s.cbin, kBinBase), kBinBase + (kBins - 1));
 }
-
-// The step within its bin, of 1024 (the bin number takes at most 10 bits of the
-// product's 24, so the steps are ordered like the tokens too).
-__device__ __forceinline__ int row_step(const Scale& s, float l) {
-    const float y = (s.lmax - l) * s.cbin;
-    return min(static_cast<int>((y - static_cast<float>(min(static_cast<int>(y), kBins - 1))) * kBins), kBins - 1);
+__device__ __forceinline__ int row_bin(const Scale& s, float l) {
+    return __float_as_int(row_place(s, l)) - __float_as_int(kBinBase);
+}
+// The step within the bin at `place`, of 1024.
+__device__ __forceinline__ int row_step(const Scale& s, float l, float place) {
+    const float part = fmaf(s.lmax - l, s.cbin, kBinBase - place);          // -1/2 .. 1/2
+    return max(0, min(static_cast<int>((part + 0.5f) * kBins), kBins - 1));
 }
 
 // Adds a token to this CTA's histogram.
@@ -252,9 +256,10 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     const int nv = n > 0 ? (n + mis + 3) >> 2 : 0;
     float4* kept = reinterpret_cast<float4*>(smem + sizeof(RowShared));
     constexpr int kBatch = KEPT ? 2 : 4;       // vectors a thread has in flight
+    const float4* vectors = reinterpret_cast<const float4*>(row - mis);
     auto fetch = [&](int i) {
+        if (i > 0 && i < nv - 1) return __ldg(vectors + i);
         const int j = 4 * i - mis;
-        if (j >= 0 && j + 4 <= n) return __ldg(reinterpret_cast<const float4*>(row + j));
         float4 v;
         v.x = j >= 0 ? __ldg(row + j) : -INFINITY;
         v.y = j + 1 >= 0 && j + 1 < n ? __ldg(row + j + 1) : -INFINITY;
@@ -365,7 +370,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     if (k <= 0 && tp >= 1.f && mp > 0.f) reach = fminf(reach, (-logf(mp) * 1.0001f + 1e-4f) * T);
     sc.reach = reach;
     sc.dmax = static_cast<double>(lmax);
-    sc.cbin = reach > 0.f ? static_cast<float>(kBins) / reach : 0.f;
+    sc.cbin = reach > 0.f ? static_cast<float>(kBins - 1) / reach : 0.f;
     if (!(sc.cbin < INFINITY)) sc.cbin = 3e38f;
     const double mp46 = static_cast<double>(mp) * kFix;
 
@@ -377,7 +382,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     auto gather = [&](u64 before, auto in) __attribute__((always_inline)) {
         if (threadIdx.x == 0) sh.seg_n[turn] = 0;
         __syncthreads();
-        each_of([&](float l, int id) { return within(sc, l) && in(l, id); }, [&](float l, int id) {
+        each_of([&](float l, int id) { return in(l, id) && within(sc, l); }, [&](float l, int id) {
             bool keep;
             const u64 m = row_mass(sh, sc, l, mp46, &keep);
             if (m == 0) return;
@@ -450,18 +455,16 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     // ---- a small top_k: counts, one list with every token that may be drawn
     if (k > 0 && k <= kCap) {
         each4([&](const float (&l)[4], int) {
-            int at[4];
-#pragma unroll
-            for (int y = 0; y < 4; ++y) at[y] = within(sc, l[y]) ? row_bin(sc, l[y]) : -1;
 #pragma unroll
             for (int y = 0; y < 4; ++y)
-                if (at[y] >= 0) atomicAdd(&sh.h[0][at[y]], 1u);
+                if (within(sc, l[y])) atomicAdd(&sh.h[0][row_bin(sc, l[y])], 1u);
         });
         hist_reduce<R, false>(sh, sh.p0, rank);
         const unsigned int all = sh.p0.cnt[kBins];
         const int bin = choose_bin(sh, sh.p0, true, min(static_cast<unsigned int>(k), all) - 1);
         if (sh.p0.cnt[bin + 1] <= kCap) {
-            gather(0, [&](float l, int) { return row_bin(sc, l) <= bin; });
+            const float last = kBinBase + bin;
+            gather(0, [&](float l, int) { return row_place(sc, l) <= last; });
             u64 z = sh.s_pre[min(k, list_n)];
             if (tp < 1.f) {
                 const u64 zp = sh.s_pre[hit_of(static_cast<u64>(static_cast<double>(tp) * static_cast<double>(z))) + 1];
@@ -526,7 +529,8 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
                 have_lo = upto <= kCap ? 0 : bin;
                 have_hi = bin;
                 list_cnt = sh.p0.cnt[have_lo];
-                gather(sh.p0.mass[have_lo], [&](float l, int) { const int x = row_bin(sc, l); return x >= have_lo && x <= bin; });
+                const float from = kBinBase + have_lo, to = kBinBase + bin;
+                gather(sh.p0.mass[have_lo], [&](float l, int) { const float x = row_place(sc, l); return x >= from && x <= to; });
             } else {
                 have_lo = 1;                   // a list of part of a bin serves no other search
                 have_hi = 0;
@@ -539,8 +543,9 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
                     const u64 m = row_mass(sh, sc, l, mp46, &keep);
                     if (m != 0) hist_add(sh, at, m);
                 };
-                each_of([&](float l, int) { return within(sc, l) && row_bin(sc, l) == bin; },
-                        [&](float l, int) { add(row_step(sc, l), l); });
+                const float place = kBinBase + bin;
+                each_of([&](float l, int) { return row_place(sc, l) == place && within(sc, l); },
+                        [&](float l, int) { add(row_step(sc, l, place), l); });
                 hist_reduce<R, true>(sh, sh.p1, rank);
                 u64 before = sh.p0.mass[bin];
                 list_cnt = sh.p0.cnt[bin];
@@ -548,7 +553,9 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
                 before += sh.p1.mass[step];
                 list_cnt += sh.p1.cnt[step];
                 unsigned int inside = sh.p1.cnt[step + 1] - sh.p1.cnt[step];
-                auto in_step = [&](float l, int) { return within(sc, l) && row_bin(sc, l) == bin && row_step(sc, l) == step; };
+                auto in_step = [&](float l, int) {
+                    return row_place(sc, l) == place && within(sc, l) && row_step(sc, l, place) == step;
+                };
                 if (inside <= kCap) {
                     gather(before, in_step);
                     return by_count ? static_cast<int>(target - list_cnt) : hit_of(target);
@@ -655,7 +662,7 @@ static int rows_keep(const float* logits, int B, int V, const float* temperature
 int launch_sample_rows(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
                        const float* top_p, const float* min_p, const float* uniforms, int32_t* out, cudaStream_t st) {
     // the widest clusters whose rows all fit on the GPU at once (two CTAs an SM): 64 rows of
-    // 128000 with top-k 36 us on clusters of 4, 49 on 8; 32 rows 26 us on 8
+    // 128000 with top-k 33 us on clusters of 4, 45 on 8; 32 rows 24 us on 8
     if (B <= 32) return rows_keep<8>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
     if (B <= 64) return rows_keep<4>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
     return rows_keep<2>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
