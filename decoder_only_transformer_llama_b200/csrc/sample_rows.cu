@@ -42,6 +42,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 1024;
 constexpr int kCap = 256;                     // tokens one list holds
 constexpr int kKept = 8192;                   // logits of a slice that stay in shared memory
+constexpr int kSlice = 65536;                 // most logits of a slice: the sums of 16 mass bits stay below 2^32
 constexpr double kFix = 70368744177664.0;     // 2^46: V * 2^46 < 2^64 for V <= 262144
 constexpr u64 kKeep = 1ull << 63;             // beside a mass: min-p keeps the token
 constexpr float kReach = 32.625f;             // 47 ln 2 = 32.58: masses beyond round to 0
@@ -664,7 +665,7 @@ int launch_sample_rows(const float* logits, int B, int V, const float* temperatu
     // the widest clusters whose rows all fit on the GPU at once (two CTAs an SM): 64 rows of
     // 128000 with top-k 33 us on clusters of 4, 45 on 8; 32 rows 24 us on 8
     if (B <= 32) return rows_keep<8>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
-    if (B <= 64) return rows_keep<4>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
+    if (B <= 64 || V > 2 * kSlice) return rows_keep<4>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
     return rows_keep<2>(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out, st);
 }
 

@@ -81,6 +81,18 @@ def test_equal_rows(llb, V):
     check(llb, lg, [1.0] * 6, [0, 10, 0, 77, 0, 0], [1.0, 1.0, 0.5, 0.3, 1.0, 0.0], [0.0, 0.0, 0.0, 0.0, 1.0, 0.0], u)
 
 
+def test_many_wide_rows_of_near_ties(llb):
+    """More than 2^17 tokens of one mass in each of many rows: a CTA's share of a
+    bin's sums must not pass 32 bits (0.5 below the maximum at T = 0.8, the 16-bit
+    parts of the mass are 0xb92b and 0xed6d)."""
+    B, V = 66, 262144
+    _, u = rows(B, 1, 41)
+    lg = torch.zeros(V)
+    lg[77777] = 0.5
+    check(llb, lg.repeat(B, 1), [0.8] * B, None, None, None, u)
+    check(llb, lg.repeat(B, 1), [0.8] * B, [200000] * B, [0.95] * B, None, u)
+
+
 def test_masked_logits(llb):
     """-inf, NaN and +inf entries, rows with one token left, rows with none."""
     lg, u = rows(12, 3000, 8)
