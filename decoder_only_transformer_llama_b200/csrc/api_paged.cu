@@ -12,6 +12,8 @@ namespace {
 bool is_dtype(int d) { return d == LLAMA_F32 || d == LLAMA_BF16 || d == LLAMA_F16; }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
+constexpr int kMaxSampleRows = 1 << 28;       // the grid holds up to 4 CTAs a row
+
 // log2(page_size), or -1 for a size that is not supported.
 int page_shift_of(int page_size) {
     for (int s = 4; s <= 8; ++s)
@@ -131,9 +133,9 @@ int llama_paged_attention(const void* q, const void* k_pages, const void* v_page
 
 int llama_sample_rows(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
                       const float* top_p, const float* min_p, const float* uniforms, int32_t* out, void* stream) {
-    if (!logits || !temperature || !uniforms || !out) return bad("logits, temperature, uniforms or out is NULL");
-    if (B < 0 || V <= 0 || V > 262144) return bad("B must be >= 0 and 0 < V <= 262144");
+    if (B < 0 || B > kMaxSampleRows || V <= 0 || V > 262144) return bad("B must be 0 .. 2^28 and V 1 .. 262144");
     if (B == 0) return LLAMA_OK;
+    if (!logits || !temperature || !uniforms || !out) return bad("logits, temperature, uniforms or out is NULL");
     return launch_sample_rows(logits, B, V, temperature, top_k, top_p, min_p, uniforms, out,
                               static_cast<cudaStream_t>(stream));
 }

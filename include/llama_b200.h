@@ -203,7 +203,7 @@ LLAMA_API int llama_sample(const float* logits, int B, int V, float temperature,
                  const float* uniforms, int32_t* out, void* stream);
 
 /* Sampling with parameters of their own for each row (a batch of requests):
- *   logits       device fp32 [B, V], V <= 262144
+ *   logits       device fp32 [B, V], B <= 2^28, V <= 262144
  *   temperature  device fp32 [B]; 0 selects the greedy argmax of that row
  *   top_k        device int32 [B] or NULL; values <= 0 or >= V keep every token
  *   top_p        device fp32 [B] or NULL; values >= 1 keep every token

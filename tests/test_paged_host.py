@@ -90,6 +90,14 @@ def test_empty_calls_launch_nothing():
     assert llb.launch_count() == n
 
 
+def test_sample_rows_of_no_rows_and_of_too_many():
+    n = llb.launch_count()
+    assert call("llama_sample_rows", ROWS, B=0, logits=None, t=None, u=None, out=None)[0] == 0    # empty tensors have no address
+    rc, msg = call("llama_sample_rows", ROWS, B=1 << 29, V=1)             # past the grid's 31 bits
+    assert rc == 1 and msg
+    assert llb.launch_count() == n
+
+
 def test_workspace_sizes():
     f = L.llama_paged_attention_workspace_bytes
     for dt in (0, 1, 2):
