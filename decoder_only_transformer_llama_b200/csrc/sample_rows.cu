@@ -15,8 +15,9 @@
 // in any order, and tokens below 2^-47 of the maximum weigh nothing.
 //
 // Measured: 1 x 32000 logits 11 us (six exchanges over the cluster, latency), 64 x 128000
-// with parameters of every kind 66 us (issue-bound: some 70 instructions per logit of a row
-// without top-k; rows with top-k 33 us), against 1.28 ms and 5.2 ms of one CTA per row
+// with parameters of every kind 62 us (rows with top-k 34, with min-p 40, with top-p 75; of
+// the histogram pass of the latter, 14 us, the additions to shared memory take 8, whose
+// lanes meet in banks, and the exponentials 4), against 1.28 ms and 5.2 ms of one CTA per row
 // with a radix select over whole-row passes.
 //
 // A row is spread over a cluster of R = 8, 4 or 2 CTAs.  A histogram over 1024 equal steps
@@ -44,6 +45,7 @@ constexpr int kCap = 256;                     // tokens one list holds
 constexpr int kKept = 8192;                   // logits of a slice that stay in shared memory
 constexpr int kSlice = 65536;                 // most logits of a slice: the sums of 16 mass bits stay below 2^32
 constexpr double kFix = 70368744177664.0;     // 2^46: V * 2^46 < 2^64 for V <= 262144
+constexpr double kOne = 4503599627370496.0;   // 2^52: adding it rounds a double to an integer, in its low 52 bits
 constexpr u64 kKeep = 1ull << 63;             // beside a mass: min-p keeps the token
 constexpr float kReach = 32.625f;             // 47 ln 2 = 32.58: masses beyond round to 0
 
@@ -51,7 +53,7 @@ struct Prefix {
     u64 mass[kBins + 1];                      // before each bin
     unsigned int cnt[kBins + 1];
 };
-struct RowShared {
+struct __align__(16) RowShared {
     unsigned int h[4][kBins];                 // this CTA's histogram: counts, mass bits 0-15, 16-31, 32-46
     Prefix p0, p1;                            // cluster totals: of the whole row, of a bin being cut
     u64 seg_key[2][kCap], seg_mass[2][kCap];  // tokens this CTA gathered, read by the cluster
@@ -64,7 +66,7 @@ struct RowShared {
     int seg_n[2];
     u64 red_a[kWarps], red_b[kWarps];
     float red_f[kWarps], red_g[kWarps];
-    double table[128];                        // 2^(-j / 128)
+    double table[32][32];                     // 2^(46 - j / 32), a column for each lane
     int bin, hit;
 };
 
@@ -96,43 +98,41 @@ __device__ __forceinline__ void st_peer32(const void* p, uint32_t rank, unsigned
     asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(cluster_addr(p, rank)), "r"(v) : "memory");
 }
 
-// One row's scales.  e = 2^(-y / 128), y = (l_max - l) * c128 with c128 = 128 log2(e) / T.
+// One row's scales.  e = 2^(-y / 32), y = (l_max - l) * c32 with c32 = 32 log2(e) / T.
 struct Scale {
-    float lmax, reach;   // distances beyond `reach` weigh nothing
-    double dmax, c128;   // l_max
+    float lmax, lcut;    // tokens below lcut weigh nothing
+    double dmax, c32;    // l_max
     float cbin;          // bins per unit of l_max - l
 };
 
-// Tokens that may weigh something (never NaN or -inf).
-__device__ __forceinline__ bool within(const Scale& s, float l) { return s.lmax - l <= s.reach; }
+constexpr double kMagic = 6755399441055744.0;    // 1.5 * 2^52: adding it rounds to an integer, in the low word
 
-// e * 2^46 at 0 <= y < 2^13 (anything elsewhere): y = n - r, |r| <= 1/2, is cut into n =
-// 128 q + j, and 2^(-y/128) = 2^-q * 2^(-j/128) * exp(r ln2 / 128) with the exponential's
-// Taylor terms up to the fourth power (|r ln2 / 128| < 0.0028: the rest is below
-// 1.3e-15, a tenth of the masses' resolution).  Table-driven exponentials after Tang (1989).
-__device__ __forceinline__ double scaled_exp(const RowShared& sh, double y) {
-    constexpr double kMagic = 6755399441055744.0;              // 1.5 * 2^52: adding it rounds to an integer
-    constexpr double c = 0.69314718055994530942 / 128.0;
-    const double t = y + kMagic;
+// Tokens that may weigh something (never NaN or -inf).
+__device__ __forceinline__ bool within(const Scale& s, float l) { return l >= s.lcut; }
+
+// A token's mass, e * 2^46 rounded to an integer, plus 2^52; for tokens within
+// reach only (others give anything).  y = n + r, |r| <= 1/2, is cut into n =
+// 32 q + j, and 2^(-y/32) = 2^-q * 2^(-j/32) * exp(-r ln2 / 32) with the exponential's
+// Taylor terms up to the fifth power (|r ln2 / 32| < 0.011: the rest is below 2.3e-15,
+// a third of the masses' resolution).  Table-driven exponentials after Tang (1989).
+// Every lane has a copy of the table in its own banks: lanes that look up different
+// entries of one copy wait for one another, 5 passes instead of 2.
+__device__ __forceinline__ double row_mass(const double* table, const Scale& s, float l) {
+    constexpr double c = 0.69314718055994530942 / 32.0;
+    const double d = s.dmax - static_cast<double>(l);
+    const double t = fma(d, s.c32, kMagic);
     const int n = __double2loint(t);
-    const double r = (t - kMagic) - y;
-    double p = fma(r, c * c * c * c / 24.0, c * c * c / 6.0);
+    const double r = fma(d, s.c32, kMagic - t);
+    double p = fma(r, -c * c * c * c * c / 120.0, c * c * c * c / 24.0);
+    p = fma(p, r, -c * c * c / 6.0);
     p = fma(p, r, c * c / 2.0);
-    p = fma(p, r, c);
+    p = fma(p, r, -c);
     p = fma(p, r, 1.0);
-    p *= sh.table[n & 127];
-    return __hiloint2double(__double2hiint(p) + (46 << 20) - ((n & ~127) << 13), __double2loint(p));   // * 2^(46 - q)
+    const double v = table[(n & 31) * 32];
+    const double scale = __hiloint2double(__double2hiint(v) - ((n & ~31) << 15), __double2loint(v));   // * 2^-q
+    return fma(p, scale, kOne);
 }
-// The mass of a logit (0 out of reach), and whether min-p keeps it (e >= mp).
-// Without branches: four of them overlap.
-__device__ __forceinline__ u64 row_mass(const RowShared& sh, const Scale& s, float l, double mp46, bool* keep) {
-    const bool in = within(s, l);
-    const double e = scaled_exp(sh, (s.dmax - static_cast<double>(l)) * s.c128);
-    *keep = in && e >= mp46;
-    const double m = e + 4503599627370496.0;                   // + 2^52: rounds to an integer in the low bits
-    const uint32_t lo = in ? __double2loint(m) : 0u, hi = in ? __double2hiint(m) & 0xfffff : 0u;
-    return (static_cast<u64>(hi) << 32) | lo;
-}
+__device__ __forceinline__ u64 mass_of(double m) { return static_cast<u64>(__double_as_longlong(m)) & 0xfffffffffffffull; }
 // A token's bin, the distance in steps rounded to an integer: as a float, 2^23 + bin
 // (ordered like the tokens; two additions and no conversion), and as a number.
 constexpr float kBinBase = 8388608.f;
@@ -148,21 +148,31 @@ __device__ __forceinline__ int row_step(const Scale& s, float l, float place) {
     return max(0, min(static_cast<int>((part + 0.5f) * kBins), kBins - 1));
 }
 
-// Adds a token to this CTA's histogram.
-__device__ __forceinline__ void hist_add(RowShared& sh, int bin, u64 m) {
-    const uint32_t lo = static_cast<uint32_t>(m), hi = static_cast<uint32_t>(m >> 32);
-    atomicAdd(&sh.h[0][bin], 1u);
-    atomicAdd(&sh.h[1][bin], lo & 0xffffu);
-    atomicAdd(&sh.h[2][bin], lo >> 16);
-    atomicAdd(&sh.h[3][bin], hi);
+// Adds a token of mass m (row_mass) to this CTA's histogram (shared address h), to its
+// counts if asked to: nothing if not `in`, without branches.
+__device__ __forceinline__ void hist_add(uint32_t h, int bin, double m, bool in, bool counted) {
+    const uint32_t lo = __double2loint(m), hi = __double2hiint(m) & 0xfffff, at = h + 4 * bin;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t@p red.shared.add.u32 [%0 + %5], %1;\n\t"
+                 "@p red.shared.add.u32 [%0 + %6], %2;\n\t@p red.shared.add.u32 [%0 + %7], %3;\n\t}"
+                 :: "r"(at), "r"(lo & 0xffffu), "r"(lo >> 16), "r"(hi), "r"(static_cast<uint32_t>(in)),
+                    "n"(4 * kBins), "n"(8 * kBins), "n"(12 * kBins) : "memory");
+    if (counted && in && (lo | hi)) asm volatile("red.shared.add.u32 [%0], 1;" :: "r"(at) : "memory");
 }
 __device__ __forceinline__ void hist_clear(RowShared& sh) {
     for (int i = threadIdx.x; i < 4 * kBins; i += kThreads) sh.h[i / kBins][i % kBins] = 0u;
 }
 
+// The most tokens that may lie in a bin of mass m (each weighs 1 at least), from the
+// smallest mass within it: 2^(46 - (bin + 1/2) step), less its rounding.
+__device__ __forceinline__ unsigned int most_tokens(u64 m, int bin, float step) {
+    const float least = exp2f(46.f - (static_cast<float>(bin) + 0.5f) * step) * 0.999f - 1.f;
+    return static_cast<unsigned int>(fminf(__ull2float_ru(m) / fmaxf(least, 1.f) * 1.0001f, 262144.f));
+}
+
 // The cluster's totals of the histograms, as sums before each bin, into `p` of every CTA.
+// step > 0: no counts were taken, the bound of most_tokens takes their place.
 template <int R, bool MASS>
-__device__ __forceinline__ void hist_reduce(RowShared& sh, Prefix& p, uint32_t rank) {
+__device__ __forceinline__ void hist_reduce(RowShared& sh, Prefix& p, uint32_t rank, float step = 0.f) {
     cluster_sync();
     {
         // CTA r adds up its share of the bins: R / 2 threads a bin, two CTAs each
@@ -182,6 +192,7 @@ __device__ __forceinline__ void hist_reduce(RowShared& sh, Prefix& p, uint32_t r
             m += __shfl_xor_sync(0xffffffffu, m, o);
             c += __shfl_xor_sync(0xffffffffu, c, o);
         }
+        if (MASS && step > 0.f) c = most_tokens(m, bin, step);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             if (MASS) st_peer64(&p.mass[bin + 1], 2 * q + x, m);
@@ -256,7 +267,6 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     const int mis = static_cast<int>((reinterpret_cast<uintptr_t>(row) >> 2) & 3);
     const int nv = n > 0 ? (n + mis + 3) >> 2 : 0;
     float4* kept = reinterpret_cast<float4*>(smem + sizeof(RowShared));
-    constexpr int kBatch = KEPT ? 2 : 4;       // vectors a thread has in flight
     const float4* vectors = reinterpret_cast<const float4*>(row - mis);
     auto fetch = [&](int i) {
         if (i > 0 && i < nv - 1) return __ldg(vectors + i);
@@ -269,26 +279,20 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         return v;
     };
     bool infinite = false;
-    // f(four logits, first id) for every vector of the slice (-inf outside it)
+    // f(four logits, first id) for every vector of the slice (-inf outside it); the next
+    // one is asked for while f works on this one.  f's code is there once: four vectors
+    // asked for and worked on together, by four copies of it, took 66 us for 62.
     auto each4 = [&](auto f) __attribute__((always_inline)) {
-        for (int i0 = threadIdx.x; i0 < nv; i0 += kBatch * kThreads) {
-            float4 v[kBatch];
+        float4 next;
+        if (threadIdx.x < nv) next = KEPT ? kept[threadIdx.x] : fetch(threadIdx.x);
+        for (int i = threadIdx.x; i < nv; i += kThreads) {
+            float l[4] = {next.x, next.y, next.z, next.w};
+            if (i + kThreads < nv) next = KEPT ? kept[i + kThreads] : fetch(i + kThreads);
+            if (infinite) {                    // only the equals of an infinite maximum weigh anything
 #pragma unroll
-            for (int x = 0; x < kBatch; ++x) {
-                const int i = i0 + x * kThreads;
-                if (i < nv) v[x] = KEPT ? kept[i] : fetch(i);
+                for (int y = 0; y < 4; ++y) l[y] = l[y] == INFINITY ? 0.f : -INFINITY;
             }
-#pragma unroll
-            for (int x = 0; x < kBatch; ++x) {
-                const int i = i0 + x * kThreads;
-                if (i >= nv) break;
-                float l[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
-                if (infinite) {                // only the equals of an infinite maximum weigh anything
-#pragma unroll
-                    for (int y = 0; y < 4; ++y) l[y] = l[y] == INFINITY ? 0.f : -INFINITY;
-                }
-                f(l, lo + 4 * i - mis);
-            }
+            f(l, lo + 4 * i - mis);
         }
     };
     // f(logit, id) for the tokens that `in` accepts
@@ -305,20 +309,30 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         });
     };
     // ---- the largest logit of the row and its smallest finite one
-    if (threadIdx.x < 128) sh.table[threadIdx.x] = exp2(-static_cast<double>(threadIdx.x) / 128.0);
+    constexpr int kAhead = KEPT ? 2 : 4;       // vectors a thread has in flight
+    float4 v[kAhead];
+    auto ask = [&](int i0) __attribute__((always_inline)) {
+#pragma unroll
+        for (int x = 0; x < kAhead; ++x) {
+            const int i = i0 + x * kThreads;
+            v[x] = i < nv ? fetch(i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+        }
+    };
+    ask(threadIdx.x);
+    {
+        const double e = exp2(46.0 - static_cast<double>(lane) / 32.0);
+#pragma unroll
+        for (int j = warp; j < 32; j += kWarps) sh.table[j][lane] = __shfl_sync(0xffffffffu, e, j);
+    }
+    const double* const table = &sh.table[0][lane];
+    const uint32_t hist = smem_u32(&sh.h[0][0]);
     hist_clear(sh);
     if (threadIdx.x == 0) { sh.hit = 0; sh.bin = 0; }
     float lmax = -INFINITY, least = INFINITY;
-    for (int i0 = threadIdx.x; i0 < nv; i0 += kBatch * kThreads) {
-        float4 v[kBatch];
+    for (int i0 = threadIdx.x; i0 < nv;) {
 #pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
-            const int i = i0 + x * kThreads;
-            v[x] = i < nv ? fetch(i) : make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-            if (KEPT && i < nv) kept[i] = v[x];                // read back by this thread only
-        }
-#pragma unroll
-        for (int x = 0; x < kBatch; ++x) {
+        for (int x = 0; x < kAhead; ++x) {
+            if (KEPT && i0 + x * kThreads < nv) kept[i0 + x * kThreads] = v[x];   // read back by this thread only
             const float l[4] = {v[x].x, v[x].y, v[x].z, v[x].w};
 #pragma unroll
             for (int y = 0; y < 4; ++y) {
@@ -326,6 +340,8 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
                 if (l[y] > -INFINITY) least = fminf(least, l[y]);
             }
         }
+        i0 += kAhead * kThreads;
+        ask(i0);
     }
     lmax = warp_max(lmax);
     least = -warp_max(-least);
@@ -364,16 +380,17 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     }
     Scale sc;
     sc.lmax = lmax;
-    sc.c128 = 128.0 * 1.4426950408889634074 / static_cast<double>(T);
-    // distances beyond `reach` weigh nothing; without top-k and top-p, neither
-    // do those that min-p drops (a little further, for its own exact test)
-    float reach = fminf(kReach * T, lmax - least);
+    sc.c32 = 32.0 * 1.4426950408889634074 / static_cast<double>(T);
+    // tokens further from the maximum than kReach * T weigh nothing; without top-k and top-p,
+    // neither do those that min-p drops (a little further, for its own exact test)
+    float reach = kReach * T;
     if (k <= 0 && tp >= 1.f && mp > 0.f) reach = fminf(reach, (-logf(mp) * 1.0001f + 1e-4f) * T);
-    sc.reach = reach;
+    sc.lcut = fmaxf(least, lmax - reach);
     sc.dmax = static_cast<double>(lmax);
+    reach = lmax - sc.lcut;
     sc.cbin = reach > 0.f ? static_cast<float>(kBins - 1) / reach : 0.f;
     if (!(sc.cbin < INFINITY)) sc.cbin = 3e38f;
-    const double mp46 = static_cast<double>(mp) * kFix;
+    const double mp52 = static_cast<double>(mp) * kFix + kOne;   // masses from here on are kept by min-p
 
     // ---- lists
     int turn = 0;                              // buffer of the next gather
@@ -384,12 +401,13 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         if (threadIdx.x == 0) sh.seg_n[turn] = 0;
         __syncthreads();
         each_of([&](float l, int id) { return in(l, id) && within(sc, l); }, [&](float l, int id) {
-            bool keep;
-            const u64 m = row_mass(sh, sc, l, mp46, &keep);
+            const double w = row_mass(table, sc, l);
+            const u64 m = mass_of(w);
             if (m == 0) return;
             const int at = atomicAdd(&sh.seg_n[turn], 1);
+            if (at >= kCap) return;            // never: the callers count or bound what they accept
             sh.seg_key[turn][at] = row_key(l, id);
-            sh.seg_mass[turn][at] = m | (keep ? kKeep : 0ull);
+            sh.seg_mass[turn][at] = m | (w >= mp52 ? kKeep : 0ull);
         });
         cluster_sync();
         // warp r copies CTA r's tokens
@@ -486,22 +504,23 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         __syncthreads();
     }
 
-    // ---- histogram of masses; the row's mass and min-p's
+    // ---- histogram of masses; the row's mass and min-p's.  Bound by shared-memory
+    // passes and integer instructions alike: counts are taken for top-k only
+    const bool counted = k > 0;
     u64 zm = 0;
     each4([&](const float (&l)[4], int) {
         if (!within(sc, fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])))) return;   // all four weigh nothing
-        u64 m[4];
-        int at[4];
+        double m[4];
 #pragma unroll
-        for (int y = 0; y < 4; ++y) {
-            bool keep;
-            m[y] = row_mass(sh, sc, l[y], mp46, &keep);
-            if (mp > 0.f && keep) zm += m[y];
-            at[y] = row_bin(sc, l[y]);
+        for (int y = 0; y < 4; ++y) m[y] = row_mass(table, sc, l[y]);
+        if (mp > 0.f) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y)
+                if (within(sc, l[y]) && m[y] >= mp52) zm += mass_of(m[y]);
         }
 #pragma unroll
         for (int y = 0; y < 4; ++y)
-            if (m[y] != 0) hist_add(sh, at[y], m[y]);
+            hist_add(hist, row_bin(sc, l[y]), m[y], within(sc, l[y]), counted);
     });
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) zm += __shfl_xor_sync(0xffffffffu, zm, o);
@@ -511,7 +530,9 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
         for (int w = 1; w < kWarps; ++w) zm += sh.red_b[w];
         sh.x_zm = zm;
     }
-    hist_reduce<R, true>(sh, sh.p0, rank);
+    // a bin's width in powers of two
+    const float step = sc.cbin > 0.f ? static_cast<float>(sc.c32 / 32.0 / static_cast<double>(sc.cbin)) : 0.f;
+    hist_reduce<R, true>(sh, sh.p0, rank, counted ? 0.f : fmaxf(step, 1e-30f));
     {
         u64 m = lane < R ? ld_peer64(&sh.x_zm, lane) : 0ull;
 #pragma unroll
@@ -539,11 +560,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
                 __syncthreads();
                 hist_clear(sh);
                 __syncthreads();
-                auto add = [&](int at, float l) {
-                    bool keep;
-                    const u64 m = row_mass(sh, sc, l, mp46, &keep);
-                    if (m != 0) hist_add(sh, at, m);
-                };
+                auto add = [&](int at, float l) { hist_add(hist, at, row_mass(table, sc, l), true, true); };
                 const float place = kBinBase + bin;
                 each_of([&](float l, int) { return row_place(sc, l) == place && within(sc, l); },
                         [&](float l, int) { add(row_step(sc, l, place), l); });
@@ -564,8 +581,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
                 // near ties: cut the step by its order keys [k0, k1]
                 u64 k1 = 0, k0 = ~0ull;
                 each_of(in_step, [&](float l, int id) {
-                    bool keep;
-                    if (row_mass(sh, sc, l, mp46, &keep) == 0) return;
+                    if (mass_of(row_mass(table, sc, l)) == 0) return;
                     const u64 key = row_key(l, id);
                     k1 = key > k1 ? key : k1;
                     k0 = key < k0 ? key : k0;
