@@ -254,7 +254,8 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     const int k = top_k ? top_k[b] : 0;
     const float tp = top_p ? top_p[b] : 1.f;
     const float mp = min_p ? min_p[b] : 0.f;
-    if (!(T >= 0.f) || T > 1e30f || !(tp >= 0.f) || !(mp >= 0.f) || mp > 1.f) {
+    // (1e30f lies above 1e30)
+    if (!(T >= 0.f) || T >= 1e30f || !(tp >= 0.f) || !(mp >= 0.f) || mp > 1.f) {
         if (rank == 0 && threadIdx.x == 0) out[b] = -1;
         return;                                // the whole cluster, before any exchange
     }

@@ -93,6 +93,19 @@ def test_many_wide_rows_of_near_ties(llb):
     check(llb, lg.repeat(B, 1), [0.8] * B, [200000] * B, [0.95] * B, None, u)
 
 
+@pytest.mark.parametrize("scale,offset,t", [
+    (1e-38, 0.0, 1.0), (1e-38, 0.0, 1e-38), (1e-44, 0.0, 1e-43), (4.0, 1e8, 0.15), (64.0, -1e8, 20.0), (1e30, 0.0, 1e30), (1e30, 0.0, 9e29),
+    (3e37, 0.0, 1e30), (3e37, 0.0, 9e29), (1e-3, 5.0, 1e30), (1e-3, 5.0, 9e29), (0.02, 0.0, 1e-4), (40.0, 0.0, 1.0), (1.0, 1e4, 1.0)])
+def test_extreme_scales(llb, scale, offset, t):
+    """Distances from denormal to overflowing, temperatures as small and as large."""
+    for V in (300, 40000, 140000):
+        lg, u = rows(5, V, 51)
+        lg = (lg / 3.0 * scale + offset).contiguous()
+        check(llb, lg, [t] * 5, None, None, None, u)
+        check(llb, lg, [t] * 5, [0, 3, 60, 290, 20000], [0.9, 0.5, 0.9, 1.0, 0.99], [0.0, 0.0, 0.1, 0.0, 0.0], u)
+        check(llb, lg, [t] * 5, None, None, [0.1, 0.5, 0.9, 0.01, 1e-30], u)
+
+
 def test_masked_logits(llb):
     """-inf, NaN and +inf entries, rows with one token left, rows with none."""
     lg, u = rows(12, 3000, 8)
