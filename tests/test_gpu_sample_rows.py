@@ -57,6 +57,20 @@ def test_every_filter(llb, V):
     check(llb, lg, t, None, None, None, u)
 
 
+@pytest.mark.parametrize("B,V", [(33, 9000), (33, 70001), (64, 40002), (65, 9000), (65, 70001), (100, 131073)])
+def test_every_filter_in_batches(llb, B, V):
+    """The narrower clusters, whose slices stay in shared memory or are read again."""
+    lg, u = rows(B, V, B + V)
+    lg[1::7] *= 0.05                                      # near ties: crowded bins
+    t = [(0.7, 1.0, 0.0, 1.6)[b % 4] for b in range(B)]
+    k = [(0, 50, 0, 3, 5000)[b % 5] for b in range(B)]
+    p = [(0.9, 1.0, 0.99)[b % 3] for b in range(B)]
+    m = [(0.0, 0.0, 0.02)[b // 3 % 3] for b in range(B)]
+    check(llb, lg, t, k, p, m, u)
+    check(llb, lg, t, None, p, None, u)
+    check(llb, lg, t, None, None, m, u)
+
+
 @pytest.mark.parametrize("u", [0.0, 1.0 - 2.0 ** -24])
 def test_ends_of_the_draw(llb, u):
     lg, _ = rows(6, 5000, 3)
