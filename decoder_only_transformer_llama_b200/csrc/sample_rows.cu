@@ -11,8 +11,9 @@
 // Z = min(Zk, Zp, Zm), and the draw is the first token whose cumulative mass
 // exceeds u * Z: it lies in the kept prefix by itself, and no filter needs
 // the identity of its last token.  Masses are fp64 exponentials held as
-// 64-bit fixed point (2^-46 resolution): every prefix sum is an exact integer
-// in any order, and tokens below 2^-47 of the maximum weigh nothing.
+// 64-bit fixed point (2^-46 resolution, 2^-45 for 2^18 tokens): every prefix sum
+// is an exact integer below 2^64 in any order, and tokens below half a unit
+// weigh nothing.
 //
 // Measured: 1 x 32000 logits 11 us (six exchanges over the cluster, latency), 64 x 128000
 // with parameters of every kind 62 us (rows with top-k 34, with min-p 40, with top-p 75; of
@@ -32,6 +33,7 @@
 // by histograms over the order key, 10 bits of it at a time.
 #include "common.cuh"
 #include "paged.h"
+#include "sample_mass.cuh"
 
 namespace llb {
 
@@ -44,7 +46,6 @@ constexpr int kBins = 1024;
 constexpr int kCap = 256;                     // tokens one list holds
 constexpr int kKept = 8192;                   // logits of a slice that stay in shared memory
 constexpr int kSlice = 65536;                 // most logits of a slice: the sums of 16 mass bits stay below 2^32
-constexpr double kFix = 70368744177664.0;     // 2^46: V * 2^46 < 2^64 for V <= 262144
 constexpr double kOne = 4503599627370496.0;   // 2^52: adding it rounds a double to an integer, in its low 52 bits
 constexpr u64 kKeep = 1ull << 63;             // beside a mass: min-p keeps the token
 constexpr float kReach = 32.625f;             // 47 ln 2 = 32.58: masses beyond round to 0
@@ -66,7 +67,7 @@ struct __align__(16) RowShared {
     int seg_n[2];
     u64 red_a[kWarps], red_b[kWarps];
     float red_f[kWarps], red_g[kWarps];
-    double table[32][32];                     // 2^(46 - j / 32), a column for each lane
+    double table[32][32];                     // 2^(mass_bits - j / 32), a column for each lane
     int bin, hit;
 };
 
@@ -110,7 +111,7 @@ constexpr double kMagic = 6755399441055744.0;    // 1.5 * 2^52: adding it rounds
 // Tokens that may weigh something (never NaN or -inf).
 __device__ __forceinline__ bool within(const Scale& s, float l) { return l >= s.lcut; }
 
-// A token's mass, e * 2^46 rounded to an integer, plus 2^52; for tokens within
+// A token's mass, e * 2^mass_bits rounded to an integer, plus 2^52; for tokens within
 // reach only (others give anything).  y = n + r, |r| <= 1/2, is cut into n =
 // 32 q + j, and 2^(-y/32) = 2^-q * 2^(-j/32) * exp(-r ln2 / 32) with the exponential's
 // Taylor terms up to the fifth power (|r ln2 / 32| < 0.011: the rest is below 2.3e-15,
@@ -163,16 +164,16 @@ __device__ __forceinline__ void hist_clear(RowShared& sh) {
 }
 
 // The most tokens that may lie in a bin of mass m (each weighs 1 at least), from the
-// smallest mass within it: 2^(46 - (bin + 1/2) step), less its rounding.
-__device__ __forceinline__ unsigned int most_tokens(u64 m, int bin, float step) {
-    const float least = exp2f(46.f - (static_cast<float>(bin) + 0.5f) * step) * 0.999f - 1.f;
+// smallest mass within it: 2^(bits - (bin + 1/2) step), less its rounding.
+__device__ __forceinline__ unsigned int most_tokens(u64 m, int bin, float step, int bits) {
+    const float least = exp2f(static_cast<float>(bits) - (static_cast<float>(bin) + 0.5f) * step) * 0.999f - 1.f;
     return static_cast<unsigned int>(fminf(__ull2float_ru(m) / fmaxf(least, 1.f) * 1.0001f, 262144.f));
 }
 
 // The cluster's totals of the histograms, as sums before each bin, into `p` of every CTA.
 // step > 0: no counts were taken, the bound of most_tokens takes their place.
 template <int R, bool MASS>
-__device__ __forceinline__ void hist_reduce(RowShared& sh, Prefix& p, uint32_t rank, float step = 0.f) {
+__device__ __forceinline__ void hist_reduce(RowShared& sh, Prefix& p, uint32_t rank, float step = 0.f, int bits = 0) {
     cluster_sync();
     {
         // CTA r adds up its share of the bins: R / 2 threads a bin, two CTAs each
@@ -192,7 +193,7 @@ __device__ __forceinline__ void hist_reduce(RowShared& sh, Prefix& p, uint32_t r
             m += __shfl_xor_sync(0xffffffffu, m, o);
             c += __shfl_xor_sync(0xffffffffu, c, o);
         }
-        if (MASS && step > 0.f) c = most_tokens(m, bin, step);
+        if (MASS && step > 0.f) c = most_tokens(m, bin, step, bits);
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
             if (MASS) st_peer64(&p.mass[bin + 1], 2 * q + x, m);
@@ -321,7 +322,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     };
     ask(threadIdx.x);
     {
-        const double e = exp2(46.0 - static_cast<double>(lane) / 32.0);
+        const double e = exp2(mass_bits(V) - static_cast<double>(lane) / 32.0);
 #pragma unroll
         for (int j = warp; j < 32; j += kWarps) sh.table[j][lane] = __shfl_sync(0xffffffffu, e, j);
     }
@@ -391,7 +392,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     reach = lmax - sc.lcut;
     sc.cbin = reach > 0.f ? static_cast<float>(kBins - 1) / reach : 0.f;
     if (!(sc.cbin < INFINITY)) sc.cbin = 3e38f;
-    const double mp52 = static_cast<double>(mp) * kFix + kOne;   // masses from here on are kept by min-p
+    const double mp52 = static_cast<double>(mp) * static_cast<double>(1ull << mass_bits(V)) + kOne;   // masses from here on are kept by min-p
 
     // ---- lists
     int turn = 0;                              // buffer of the next gather
@@ -406,23 +407,24 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
             const u64 m = mass_of(w);
             if (m == 0) return;
             const int at = atomicAdd(&sh.seg_n[turn], 1);
-            if (at >= kCap) return;            // never: the callers count or bound what they accept
+            if (at >= kCap) return;            // never: the callers count or bound what they accept,
+                                               // and the lists are cut at kCap here and below
             sh.seg_key[turn][at] = row_key(l, id);
             sh.seg_mass[turn][at] = m | (w >= mp52 ? kKeep : 0ull);
         });
         cluster_sync();
         // warp r copies CTA r's tokens
-        int at = lane < R ? static_cast<int>(ld_peer32(&sh.seg_n[turn], lane)) : 0;
+        int at = lane < R ? min(static_cast<int>(ld_peer32(&sh.seg_n[turn], lane)), kCap) : 0;
         const int mine = __shfl_sync(0xffffffffu, at, warp & (R - 1));
 #pragma unroll
         for (int o = 1; o < R; o <<= 1) {
             const int y = __shfl_up_sync(0xffffffffu, at, o);
             if (lane >= o) at += y;
         }
-        list_n = __shfl_sync(0xffffffffu, at, R - 1);
+        list_n = min(__shfl_sync(0xffffffffu, at, R - 1), kCap);
         at = __shfl_sync(0xffffffffu, at, warp & (R - 1)) - mine;
         if (warp < R)
-            for (int i = lane; i < mine; i += 32) {
+            for (int i = lane; i < min(mine, kCap - at); i += 32) {
                 const u64 key = ld_peer64(&sh.seg_key[turn][i], warp), m = ld_peer64(&sh.seg_mass[turn][i], warp);
                 sh.key[at + i] = key;
                 sh.mass[at + i] = m;
@@ -533,7 +535,7 @@ sample_rows_kernel(const float* __restrict__ logits, int V, const float* __restr
     }
     // a bin's width in powers of two
     const float step = sc.cbin > 0.f ? static_cast<float>(sc.c32 / 32.0 / static_cast<double>(sc.cbin)) : 0.f;
-    hist_reduce<R, true>(sh, sh.p0, rank, counted ? 0.f : fmaxf(step, 1e-30f));
+    hist_reduce<R, true>(sh, sh.p0, rank, counted ? 0.f : fmaxf(step, 1e-30f), mass_bits(V));
     {
         u64 m = lane < R ? ld_peer64(&sh.x_zm, lane) : 0ull;
 #pragma unroll
