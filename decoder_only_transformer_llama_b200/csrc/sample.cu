@@ -13,18 +13,18 @@
 // row (which also gives the total mass) serves both selects, and once a chosen
 // digit prefix holds at most kListCap keys they are copied into shared memory
 // and the remaining passes read only them.  Masses are e_i = exp((l_i - l_max)/T)
-// evaluated in fp64 and held as 64-bit fixed point (2^-46 resolution), so
-// every prefix sum is an exact integer and the result does not depend on the
-// summation order.
+// evaluated in fp64 and held as 64-bit fixed point (2^-46 resolution, 2^-45 for
+// 2^18 tokens: mass_bits), so every prefix sum is an exact integer below 2^64 and
+// the result does not depend on the summation order.
 #include "common.cuh"
 #include "model.h"
+#include "sample_mass.cuh"
 
 namespace llb {
 
 namespace {
 constexpr int kSampleThreads = 1024;
 constexpr int kWarps = kSampleThreads / 32;
-constexpr double kFixScale = 70368744177664.0;    // 2^46: V * 2^46 < 2^64 for V <= 262144
 }
 
 __device__ __forceinline__ uint32_t ordered_bits(float f) {
@@ -102,9 +102,12 @@ struct TopPShared {
     float lmax;
 };
 
-__device__ __forceinline__ unsigned long long fixed_mass(float l, double lmax, double inv_t) {
+// The scale of the masses of a row of V tokens.
+__device__ __forceinline__ double fix_scale(int V) { return static_cast<double>(1ull << mass_bits(V)); }
+
+__device__ __forceinline__ unsigned long long fixed_mass(float l, double lmax, double inv_t, double scale) {
     const double e = exp((static_cast<double>(l) - lmax) * inv_t);
-    return static_cast<unsigned long long>(e * kFixScale + 0.5);
+    return static_cast<unsigned long long>(e * scale + 0.5);
 }
 
 // Per-warp histograms of digit (key >> shift) & 255 over the keys that match
@@ -146,7 +149,7 @@ __device__ void digit_histogram(TopPShared& sh, const float* row, int V, bool fr
         for (int i = threadIdx.x; i < V; i += blockDim.x) {
             const float l = row[i];
             const uint64_t key = sort_key(l, i);
-            if ((key & mask) == prefix) add(key, fixed_mass(l, lmax, inv_t));
+            if ((key & mask) == prefix) add(key, fixed_mass(l, lmax, inv_t, fix_scale(V)));
         }
     }
     if (cur >= 0) {
@@ -235,7 +238,7 @@ __device__ void compact(TopPShared& sh, const float* row, int V, double lmax, do
         if ((key & mask) == prefix) {
             const int j = atomicAdd(&sh.list_n, 1);
             sh.list_key[j] = key;
-            sh.list_mass[j] = fixed_mass(l, lmax, inv_t);
+            sh.list_mass[j] = fixed_mass(l, lmax, inv_t, fix_scale(V));
         }
     }
     __syncthreads();
@@ -330,7 +333,7 @@ top_p_kernel(const float* __restrict__ logits, int V, float temperature, float t
     unsigned long long before_edge;
     const uint64_t edge = radix_select(sh, row, V, lmax, inv_t, t1, &list_prefix, &before_edge);
     const int edge_id = static_cast<int>(~static_cast<uint32_t>(edge & 0xffffffffu));
-    const unsigned long long Z = before_edge + fixed_mass(row[edge_id], lmax, inv_t);
+    const unsigned long long Z = before_edge + fixed_mass(row[edge_id], lmax, inv_t, fix_scale(V));
 
     // draw: first kept key whose inclusive mass exceeds u * Z
     double u = static_cast<double>(uniforms[b]);
@@ -536,7 +539,7 @@ top_p_cluster_kernel(const float* __restrict__ logits, int V, float temperature,
     for (int j = threadIdx.x; j < n; j += blockDim.x) {
         const float l = row[lo + j];
         ob[j] = ordered_bits(l);
-        mass[j] = fixed_mass(l, lmax, inv_t);
+        mass[j] = fixed_mass(l, lmax, inv_t, fix_scale(V));
     }
     __syncthreads();
     int k = 0;
@@ -557,7 +560,7 @@ top_p_cluster_kernel(const float* __restrict__ logits, int V, float temperature,
     unsigned long long before_edge;
     const uint64_t edge = tp_select(sh, ob, mass, n, lo, t1, k, &before_edge);
     const int edge_id = static_cast<int>(~static_cast<uint32_t>(edge & 0xffffffffu));
-    const unsigned long long Z = before_edge + fixed_mass(row[edge_id], lmax, inv_t);
+    const unsigned long long Z = before_edge + fixed_mass(row[edge_id], lmax, inv_t, fix_scale(V));
 
     // draw: first kept key whose inclusive mass exceeds u * Z
     double u = static_cast<double>(uniforms[b]);

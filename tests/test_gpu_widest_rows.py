@@ -72,3 +72,15 @@ def test_ordinary_widest_rows(llb, B):
     check(llb, lg, t, k, p, m, u)
     check(llb, lg, t, None, p, None, u)
     check(llb, lg, t, None, None, m, u)
+
+
+@pytest.mark.parametrize("V", [WIDEST - 1, WIDEST])
+def test_llama_sample_of_full_masses(llb, V):
+    """The scalar sampler on the same rows: equal logits, and distinct ones of equal mass."""
+    distinct, _ = rows(6, V, 29)
+    for lg, t in ((torch.full((6, V), -2.25), 0.8), (distinct, 9e29)):
+        d, u = lg.cuda(), uniforms(6)
+        for p in (0.3, 0.9, 1.0):
+            out = torch.full((6,), -5, dtype=torch.int32, device="cuda")
+            llb.sample(d, t, p, torch.tensor(u).cuda(), out)
+            assert out.tolist() == [R.sample(lg[b], f32(t), 0, f32(p), 0.0, f32(u[b])) for b in range(6)]
