@@ -114,7 +114,8 @@ template <typename T> __device__ __forceinline__ bool not_finite16(uint32_t h) {
 // everything it needs at once.  With `out` the rows are finished: row r of the
 // tile lies at out + (r >> lrep) * token + (r & (2^lrep - 1)) * HD and sees lim0 +
 // (r >> lrep) keys; without it the merged partial result takes the place of the
-// first one (a row's threads lie in one warp, so all have read it).
+// first one: a row's threads lie in one warp, which all goes through the loop
+// together and has read the first one's (m, l) before one lane overwrites it.
 template <typename T, int HD>
 __device__ __forceinline__ void merge_tile(float2* part_ml, float* part_o, int cf, int first, int n, int stride, int rows,
                                            T* out, int lrep, long long token, int lim0) {
@@ -122,8 +123,11 @@ __device__ __forceinline__ void merge_tile(float2* part_ml, float* part_o, int c
         const int x = first + k * stride;
         return static_cast<long long>(2 * x + (x == cf ? 1 : 0)) * kRows;
     };
+    static_assert(HD / 4 <= 32 && kThreads % 32 == 0, "a row's threads lie in one warp");
+    const int all = rows * (HD / 4);
 #pragma unroll 2
-    for (int idx = threadIdx.x; idx < rows * (HD / 4); idx += kThreads) {
+    for (int idx = threadIdx.x; (idx & ~31) < all; idx += kThreads) {
+        const bool in = idx < all;                // the same number of turns for a whole warp
         const int r = idx / (HD / 4), d = (idx % (HD / 4)) * 4;
         float2 ml[kFan];
         float4 v[kFan];
@@ -131,7 +135,7 @@ __device__ __forceinline__ void merge_tile(float2* part_ml, float* part_o, int c
         for (int k = 0; k < kFan; ++k) {
             ml[k] = make_float2(-INFINITY, 0.f);
             v[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (k < n) {
+            if (k < n && in) {
                 ml[k] = __ldcg(part_ml + slot_of(k) + r);
                 v[k] = __ldcg(reinterpret_cast<const float4*>(part_o + (slot_of(k) + r) * HD + d));
             }
@@ -150,10 +154,12 @@ __device__ __forceinline__ void merge_tile(float2* part_ml, float* part_o, int c
             o.z = fmaf(v[k].z, f, o.z); o.w = fmaf(v[k].w, f, o.w);
         }
         if (!out) {
-            *reinterpret_cast<float4*>(part_o + (slot_of(0) + r) * HD + d) = o;
-            if (d == 0) part_ml[slot_of(0) + r] = make_float2(M, L);
+            __syncwarp();                         // every lane has read the first one's (m, l)
+            if (in) *reinterpret_cast<float4*>(part_o + (slot_of(0) + r) * HD + d) = o;
+            if (in && d == 0) part_ml[slot_of(0) + r] = make_float2(M, L);
             continue;
         }
+        if (!in) continue;
         T* dst = out + (r >> lrep) * token + (r & ((1 << lrep) - 1)) * HD + d;
         const float4 y = lim0 + (r >> lrep) > 0 ? make_float4(o.x / L, o.y / L, o.z / L, o.w / L)
                                                 : make_float4(0.f, 0.f, 0.f, 0.f);
