@@ -640,27 +640,32 @@ static int attn_go(const PagedAttnArgs& a, cudaStream_t st) {
     constexpr int ring = kStages * 2 * KU * HD * static_cast<int>(sizeof(T));
     constexpr int scr = sizeof(T) == 2 ? 4 * 4 * HD * 4 : kRows * HD * 4 + kRows * KU * 4;
     // the work list's room, in three sizes so that the occupancy is asked once for each
-    const int bucket = a.B <= 64 ? 0 : a.B <= 256 ? 1 : 2;
-    const int room = bucket == 0 ? 64 : bucket == 1 ? 256 : kPagedMaxRequests;
-    const int smem = ring + scr + (room + 1) * 8 + room * static_cast<int>(sizeof(WorkReq));
+    constexpr int rooms[3] = {64, 256, kPagedMaxRequests};
+    const int bucket = a.B <= rooms[0] ? 0 : a.B <= rooms[1] ? 1 : 2;
+    auto smem_of = [](int room) { return ring + scr + (room + 1) * 8 + room * static_cast<int>(sizeof(WorkReq)); };
+    const int smem = smem_of(rooms[bucket]);
     auto kern = paged_attn_kernel<T, HD>;
-    static int sms = 0, resident[3] = {0, 0, 0};
-    if (resident[bucket] == 0) {
-        int dev = 0, n = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged_attn_kernel)");
-        resident[bucket] = n < 1 ? 1 : n;
-    }
+    struct Fit { int sms, resident[3]; };
+    static PerDevice<Fit> per_device;
+    Fit fit;
+    const cudaError_t e = per_device.get(&fit, [&](int dev, Fit* f) {
+        cudaError_t r = cudaDeviceGetAttribute(&f->sms, cudaDevAttrMultiProcessorCount, dev);
+        if (r == cudaSuccess) r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
+        for (int i = 0; i < 3 && r == cudaSuccess; ++i) {
+            int n = 0;
+            r = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, kThreads, smem_of(rooms[i]));
+            f->resident[i] = n < 1 ? 1 : n;
+        }
+        return r;
+    });
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged_attn_kernel)");
     const int rep = a.nh / a.nkv;
     TileShape shape;
     shape.lr = rep == 1 ? 4 : rep == 2 ? 3 : rep == 4 ? 2 : 1;
     shape.lk = KU == 64 ? 6 : 5;
     // one resident wave, and no more CTAs than the step can have units
     const long long cap = ((static_cast<long long>(a.max_pages) << a.page_shift) + KU - 1) / KU;
-    long long grid = static_cast<long long>(sms) * resident[bucket];
+    long long grid = static_cast<long long>(fit.sms) * fit.resident[bucket];
     if (grid > kMaxCtas) grid = kMaxCtas;
     const long long most = static_cast<long long>(a.T) * a.nkv * cap;
     if (grid > most) grid = most;

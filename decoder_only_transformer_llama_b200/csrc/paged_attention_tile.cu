@@ -689,12 +689,13 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
 // ---------------------------------------------------------------- host side
 
 namespace {
-PFN_cuTensorMapEncodeTiled_v12000 g_encode3 = nullptr;
+std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode3{nullptr};
 
 // A 3-d map of 16-bit values, boxes of 64 x b1 x b2, 128-byte swizzle.
 int encode_3d(CUtensorMap* map, const void* base, int dtype, long long d0, long long d1, long long d2, long long s1,
               long long s2, int b1, int b2) {
-    if (!g_encode3) {
+    PFN_cuTensorMapEncodeTiled_v12000 encode = g_encode3.load(std::memory_order_relaxed);
+    if (!encode) {
         void* fn = nullptr;
         cudaDriverEntryPointQueryResult q;
         cudaError_t e = cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &fn, cudaEnableDefault, &q);
@@ -702,15 +703,17 @@ int encode_3d(CUtensorMap* map, const void* base, int dtype, long long d0, long 
             set_error("cuTensorMapEncodeTiled unavailable");
             return LLAMA_ERR_CUDA;
         }
-        g_encode3 = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+        encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+        g_encode3.store(encode, std::memory_order_relaxed);
     }
     const cuuint64_t dims[3] = {static_cast<cuuint64_t>(d0), static_cast<cuuint64_t>(d1), static_cast<cuuint64_t>(d2)};
     const cuuint64_t strides[2] = {static_cast<cuuint64_t>(s1) * 2, static_cast<cuuint64_t>(s2) * 2};
     const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(b1), static_cast<cuuint32_t>(b2)};
     const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = g_encode3(map, dtype == LLAMA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3,
-                                 const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                 CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const CUtensorMapDataType type = dtype == LLAMA_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUresult r = encode(map, type, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) {
         set_error("cuTensorMapEncodeTiled failed (%d) for a paged cache", static_cast<int>(r));
         return LLAMA_ERR_CUDA;
@@ -736,15 +739,16 @@ static int tile_go(const PagedAttnArgs& a, int dtype, cudaStream_t st) {
     int nslots = (most - 1024 - 2 * TILE - list) / TILE;
     if (nslots > kMaxSlots) nslots = kMaxSlots;
     const int smem = 1024 + (2 + nslots) * TILE + list;
-    static int sms = 0;
-    if (sms == 0) {
-        int dev = 0, n = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
-        if (e == cudaSuccess) e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged_attn_tile_kernel)");
-        sms = n < kMaxCtas ? n : kMaxCtas;
-    }
+    static PerDevice<int> per_device;
+    int sms = 0;
+    const cudaError_t e = per_device.get(&sms, [&](int dev, int* out) {
+        int n = 0;
+        cudaError_t r = cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+        if (r == cudaSuccess) r = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+        *out = n < kMaxCtas ? n : kMaxCtas;
+        return r;
+    });
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(paged_attn_tile_kernel)");
     TileShape shape;
     shape.lr = rep == 1 ? 8 : rep == 2 ? 7 : rep == 4 ? 6 : 5;
     shape.lk = 7;

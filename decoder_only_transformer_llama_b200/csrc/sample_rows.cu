@@ -646,12 +646,13 @@ template <int R, bool KEPT>
 static int rows_go(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
                    const float* top_p, const float* min_p, const float* uniforms, int32_t* out, cudaStream_t st) {
     constexpr int most = static_cast<int>(sizeof(RowShared)) + (KEPT ? (kKept + 4) * 4 : 0);
-    static bool attr = false;
-    if (!attr) {
-        cudaError_t e = cudaFuncSetAttribute(sample_rows_kernel<R, KEPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
-        if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(sample_rows_kernel)");
-        attr = true;
-    }
+    static PerDevice<int> per_device;          // the attribute's value
+    int room = 0;
+    cudaError_t e = per_device.get(&room, [&](int, int* out) {
+        *out = most;
+        return cudaFuncSetAttribute(sample_rows_kernel<R, KEPT>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
+    });
+    if (e != cudaSuccess) return cuda_fail(e, "cudaFuncSetAttribute(sample_rows_kernel)");
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(B * R);
     cfg.blockDim = dim3(kThreads);
@@ -665,7 +666,7 @@ static int rows_go(const float* logits, int B, int V, const float* temperature, 
     at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = 1;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, sample_rows_kernel<R, KEPT>, logits, V, temperature, top_k, top_p, min_p,
+    e = cudaLaunchKernelEx(&cfg, sample_rows_kernel<R, KEPT>, logits, V, temperature, top_k, top_p, min_p,
                                        uniforms, out);
     count_launch();
     if (e != cudaSuccess) return cuda_fail(e, "sample_rows_kernel");

@@ -37,7 +37,9 @@
  *     reads the SM count on the device current at that time, and later
  *     launches reuse them; a second device in the same process is not
  *     supported (its large-shared-memory launches may fail with
- *     LLAMA_ERR_CUDA).
+ *     LLAMA_ERR_CUDA).  llama_sample_rows and the paged-cache operators of
+ *     llama_b200_ops.h look these up on each device: they run on whichever
+ *     device is current, from any host thread.
  */
 #ifndef LLAMA_B200_H
 #define LLAMA_B200_H
