@@ -35,6 +35,11 @@ from . import Model, sample, sample_rows, token_logprobs
 PAD = -1
 
 
+def _number(value):
+    """A tensor or array of one value as a number, anything else as it is."""
+    return value.item() if hasattr(value, "shape") and int(np.prod(value.shape)) == 1 else value
+
+
 def generate(model: Model, prompts: Sequence[Sequence[int]], max_gen_len: Optional[int] = None,
              temperature: Union[float, Sequence[float]] = 0.6, top_p: Union[float, Sequence[float]] = 0.9,
              uniforms=None, logprobs: bool = False, echo: bool = False, eos_id: Optional[int] = None,
@@ -44,9 +49,9 @@ def generate(model: Model, prompts: Sequence[Sequence[int]], max_gen_len: Option
 
     uniforms: device fp32 tensor [>= total_len, len(prompts)], needed when a
     temperature is > 0.  temperature, top_p, top_k (0: off) and min_p (0: off)
-    are one value or one per prompt; with top_k, min_p or any list each step
-    samples with llama_sample_rows.  Returns (token lists, log-probability
-    lists or None)."""
+    are one value (a number, or a tensor or array of one) or one per prompt;
+    with top_k, min_p or one value per prompt each step samples with
+    llama_sample_rows.  Returns (token lists, log-probability lists or None)."""
     import torch
 
     a = model.args
@@ -68,6 +73,7 @@ def generate(model: Model, prompts: Sequence[Sequence[int]], max_gen_len: Option
             raise ValueError(f"{name} has {len(rows)} entries for {B} prompts")
         return rows
 
+    temperature, top_p, top_k, min_p = (_number(v) for v in (temperature, top_p, top_k, min_p))
     by_row = top_k is not None or min_p is not None or not (np.isscalar(temperature) and np.isscalar(top_p))
     temps = per_row(temperature, 0.0, "temperature")
     if by_row:
