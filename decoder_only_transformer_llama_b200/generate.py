@@ -26,6 +26,7 @@ The driver only moves data and makes the per-step decisions the loop makes on
 the host (keep the prompt token, track EOS); every forward pass, every sampled
 token and every log-probability is computed by the library's kernels.
 """
+import math
 from typing import List, Optional, Sequence, Tuple, Union
 
 import numpy as np
@@ -77,9 +78,15 @@ def generate(model: Model, prompts: Sequence[Sequence[int]], max_gen_len: Option
     by_row = top_k is not None or min_p is not None or not (np.isscalar(temperature) and np.isscalar(top_p))
     temps = per_row(temperature, 0.0, "temperature")
     if by_row:
-        params = [torch.tensor(v, dtype=t, device=dev) for v, t in
+        params = [torch.tensor(v, dtype=t) for v, t in
                   ((temps, torch.float32), (per_row(top_k, 0, "top_k"), torch.int32),
                    (per_row(top_p, 1.0, "top_p"), torch.float32), (per_row(min_p, 0.0, "min_p"), torch.float32))]
+        # what the sampler answers with -1 for, known before the first forward
+        for name, v, most in (("temperature", params[0], 1e30), ("top_p", params[2], math.inf), ("min_p", params[3], 1.0)):
+            fine = (v >= 0) & (v.double() <= most)
+            if not fine.all():
+                raise ValueError(f"{name} of prompt {int((~fine).nonzero()[0])} is out of range")
+        params = [v.to(dev) for v in params]
         greedy_u = torch.zeros(B, dtype=torch.float32, device=dev)
     if max(temps) > 0 and (uniforms is None or uniforms.shape[0] < total or uniforms.shape[1] != B):
         raise ValueError(f"sampling needs uniforms of shape [>= {total}, {B}]")
@@ -133,8 +140,6 @@ def generate(model: Model, prompts: Sequence[Sequence[int]], max_gen_len: Option
         else:
             sample(last_lg, 0.0, top_p, None, nxt)
         chosen = nxt.cpu().numpy().astype(np.int64)
-        if chosen.min() < 0:
-            raise ValueError(f"sampling parameters of prompt {int(chosen.argmin())} are out of range")
         tok[:, cur] = np.where(in_prompt[:, cur], tok[:, cur], chosen)
         if logprobs:
             logprobs_of(rows, prev + 1, cur + 1)

@@ -1,6 +1,8 @@
 """The forms in which generate takes its sampling parameters, on the CPU with
 stand-ins for the model and the samplers: numbers, tensors and arrays of one
 value, and one value per prompt."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -50,3 +52,22 @@ def test_one_value_beside_a_list(run):
     assert kinds == {"rows"}
     assert run(temperature=torch.tensor(0.75), top_p=np.array(0.875), top_k=torch.tensor(7))[0] == want
     assert run(temperature=torch.tensor([0.75, 0.75]), top_p=np.array([0.875, 0.875]), top_k=np.array([7, 7]))[0] == want
+
+
+@pytest.mark.parametrize("kw,name", [
+    (dict(temperature=[0.5, -1.0]), "temperature of prompt 1"), (dict(temperature=[math.nan, 0.5]), "temperature of prompt 0"),
+    (dict(temperature=[0.5, 1e31]), "temperature of prompt 1"), (dict(temperature=math.inf, top_k=4), "temperature of prompt 0"),
+    (dict(temperature=float(torch.tensor(1e30)), top_k=4), "temperature of prompt 0"),
+    (dict(top_p=[0.9, -0.1]), "top_p of prompt 1"), (dict(top_p=[math.nan, 0.1]), "top_p of prompt 0"),
+    (dict(min_p=1.5), "min_p of prompt 0"), (dict(min_p=[0.0, -0.5]), "min_p of prompt 1"),
+    (dict(min_p=[0.5, math.nan]), "min_p of prompt 1")])
+def test_bad_values_are_refused_before_the_first_forward(run, monkeypatch, kw, name):
+    monkeypatch.setattr(T._Model, "prefill", lambda *a, **k: pytest.fail("a forward ran"))
+    with pytest.raises(ValueError, match=name + " is out of range"):
+        run(**kw)
+
+
+@pytest.mark.parametrize("kw", [dict(top_p=[0.5, 7.0]), dict(top_p=[math.inf, 0.0]), dict(min_p=[0.0, 1.0]),
+                                dict(temperature=[9e29, 0.0]), dict(top_k=[-3, 1000])])
+def test_ends_of_the_ranges_are_taken(run, kw):
+    assert run(**kw)[1] == {"rows"}
