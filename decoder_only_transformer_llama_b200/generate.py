@@ -88,7 +88,8 @@ def generate(model: Model, prompts: Sequence[Sequence[int]], max_gen_len: Option
                 raise ValueError(f"{name} of prompt {int((~fine).nonzero()[0])} is out of range")
         params = [v.to(dev) for v in params]
         greedy_u = torch.zeros(B, dtype=torch.float32, device=dev)
-    if max(temps) > 0 and (uniforms is None or uniforms.shape[0] < total or uniforms.shape[1] != B):
+    draws = max(temps) > 0
+    if draws and (uniforms is None or uniforms.shape[0] < total or uniforms.shape[1] != B):
         raise ValueError(f"sampling needs uniforms of shape [>= {total}, {B}]")
 
     tok = np.full((B, total), PAD, dtype=np.int64)
@@ -133,7 +134,7 @@ def generate(model: Model, prompts: Sequence[Sequence[int]], max_gen_len: Option
             model.decode_step(x, pos, logits=last_lg)
             rows = last_lg
         if by_row:
-            sample_rows(last_lg, params[0], greedy_u if uniforms is None else uniforms[cur].contiguous(), nxt,
+            sample_rows(last_lg, params[0], uniforms[cur].contiguous() if draws else greedy_u, nxt,
                         top_k=params[1], top_p=params[2], min_p=params[3])
         elif temperature > 0:
             sample(last_lg, temperature, top_p, uniforms[cur].contiguous(), nxt)

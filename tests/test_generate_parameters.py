@@ -71,3 +71,11 @@ def test_bad_values_are_refused_before_the_first_forward(run, monkeypatch, kw, n
                                 dict(temperature=[9e29, 0.0]), dict(top_k=[-3, 1000])])
 def test_ends_of_the_ranges_are_taken(run, kw):
     assert run(**kw)[1] == {"rows"}
+
+
+@pytest.mark.parametrize("uniforms", [torch.rand(1, 2), torch.rand(24, 5), torch.rand(3)])
+def test_greedy_rows_read_no_uniforms(run, uniforms):
+    """As the scalar path: at temperature 0 the tensor is not looked at, whatever its shape."""
+    want, _ = run(temperature=0.0, uniforms=uniforms)
+    for kw in (dict(temperature=[0.0, 0.0]), dict(temperature=0.0, top_k=5), dict(temperature=0.0, min_p=0.1)):
+        assert run(uniforms=uniforms, **kw) == (want, {"rows"})
