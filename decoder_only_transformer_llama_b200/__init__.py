@@ -44,7 +44,7 @@ EXPORTED = ("llama_model_bytes", "llama_model_create", "llama_set_weight", "llam
             "llama_tp_prefill_all", "llama_tp_decode_step_all", "llama_tp_buffers", "llama_tp_bind",
             "llama_paged_plan", "llama_rope_table", "llama_paged_append", "llama_paged_attention_workspace_bytes",
             "llama_paged_attention", "llama_sample_rows")
-LLAMA_STALL_NONE, LLAMA_STALL_PROJECTION, LLAMA_STALL_ATTENTION = 0, 1, 2
+LLAMA_STALL_NONE, LLAMA_STALL_PROJECTION, LLAMA_STALL_ATTENTION, LLAMA_STALL_PAGED = 0, 1, 2, 3
 TIMELINE_KINDS = {0: "embed", 1: "projection", 2: "attention", 3: "sample", 4: "rmsnorm"}
 
 
@@ -796,6 +796,14 @@ def paged_attention(q, k_pages, v_pages, block_tables, cu_new, seq_lens, out, ma
     if rc:
         _check(rc)
     return out
+
+
+def paged_debug_stall(stage: int = 0, wait_limit_ns: int = 1_000_000):
+    """Arm a one-shot stalled producer in the next paged_attention call of this
+    process that takes the chunk kernel (stage -1: disarm): tests of the device
+    timeout (llama_debug_stall without a model)."""
+    _check(_lib.llama_debug_stall(None, LLAMA_STALL_NONE if stage == -1 else LLAMA_STALL_PAGED, int(stage),
+                                  int(wait_limit_ns)))
 
 
 def sample_rows(logits, temperature, uniforms, out, top_k=None, top_p=None, min_p=None, stream=None):

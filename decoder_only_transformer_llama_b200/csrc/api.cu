@@ -10,6 +10,7 @@
 
 #include "common.cuh"
 #include "model.h"
+#include "paged.h"
 #include "../../include/llama_b200_ops.h"
 
 namespace llb {
@@ -1035,14 +1036,19 @@ int llama_model_destroy(llama_model* m) {
 }
 
 int llama_debug_stall(llama_model* m, int which, int unit, int64_t wait_limit_ns) {
-    if (!m) { set_error("model is NULL"); return LLAMA_ERR_INVALID_ARG; }
-    if (which != LLAMA_STALL_NONE && which != LLAMA_STALL_PROJECTION && which != LLAMA_STALL_ATTENTION) {
-        set_error("which must be LLAMA_STALL_NONE, _PROJECTION or _ATTENTION");
+    const bool paged = !m && (which == LLAMA_STALL_NONE || which == LLAMA_STALL_PAGED);   // the kernel without a model
+    if (!m && !paged) { set_error("model is NULL"); return LLAMA_ERR_INVALID_ARG; }
+    if (!paged && which != LLAMA_STALL_NONE && which != LLAMA_STALL_PROJECTION && which != LLAMA_STALL_ATTENTION) {
+        set_error("which must be LLAMA_STALL_NONE, _PROJECTION or _ATTENTION (_PAGED without a model)");
         return LLAMA_ERR_INVALID_ARG;
     }
     if (which != LLAMA_STALL_NONE && (unit < 0 || wait_limit_ns < 1000 || wait_limit_ns > 2000000000LL)) {
         set_error("unit must be >= 0 and the wait limit between 1 us and 2 s");
         return LLAMA_ERR_INVALID_ARG;
+    }
+    if (paged) {
+        arm_paged_stall(which == LLAMA_STALL_PAGED ? unit : -1, wait_limit_ns);
+        return LLAMA_OK;
     }
     if (which != LLAMA_STALL_NONE && m->dtype == LLAMA_F32) {
         set_error("the stall is a feature of the 16-bit decode kernels");

@@ -72,6 +72,8 @@ size_t paged_attention_ws(int nh, int nkv, int hd, int dtype, int max_new);
 // Chunks on tcgen05 (16-bit caches, head_dim 64 or 128, scale > 0).
 size_t paged_attention_tile_ws(int hd);
 int launch_paged_attention_tile(const PagedAttnArgs& a, int dtype, cudaStream_t st);
+// The next launch of that kernel, by any thread, stalls stage `stage` of CTA 0 (llama_debug_stall); -1: none.
+void arm_paged_stall(int stage, long long wait_ns);
 int launch_paged_attention(const PagedAttnArgs& a, int dtype, cudaStream_t st);
 int launch_sample_rows(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
                        const float* top_p, const float* min_p, const float* uniforms, int32_t* out, cudaStream_t st);

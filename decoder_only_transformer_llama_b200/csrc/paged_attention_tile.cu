@@ -142,8 +142,8 @@ __device__ __forceinline__ void warp_commit(uint64_t* bar) {
         "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
         :: "r"(smem_u32(bar)) : "memory");
 }
-__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, mbar_wait(bar, parity));
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, uint64_t limit) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit));
 }
 template <typename T> __device__ __forceinline__ bool not_finite16(uint32_t h) {
     constexpr uint32_t e = std::is_same<T, bf16>::value ? 0x7f80u : 0x7c00u;
@@ -224,6 +224,13 @@ __device__ __noinline__ void merge_half(float2* part_ml, float4* part_o, int cf,
     }
 }
 
+// Every wait's limit and, in tests of it (llama_debug_stall), the stage of CTA
+// 0's run, counted from 1, whose copies never come.
+struct Waits {
+    uint64_t limit;
+    int stalled;
+};
+
 // A part of one tile that a CTA works on: units c.j .. c.j + len - 1.
 struct Segment {
     WorkCur c;
@@ -234,7 +241,8 @@ struct Segment {
 template <typename T, int HD>
 __global__ void __launch_bounds__(kThreads, 1)
 paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_constant__ CUtensorMap mapK,
-                       const __grid_constant__ CUtensorMap mapV, PagedAttnArgs a, TileShape shape, int nslots) {
+                       const __grid_constant__ CUtensorMap mapV, PagedAttnArgs a, TileShape shape, int nslots,
+                       Waits waits) {
     constexpr int NB = HD / 64;                    // boxes per tile
     // fp16 loses relative precision below 2^-14: weights, up to 2^8 before m moves,
     // carry a factor 2^7 there
@@ -321,7 +329,7 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
             const WorkReq r = req[sg.c.b];
             const int t0 = sg.c.tile << shape.lr;
             const bool two = two_halves(sg);
-            ok = __all_sync(0xffffffffu, mbar_wait(&q_empty, (nseg & 1) ^ 1));
+            ok = __all_sync(0xffffffffu, mbar_wait(&q_empty, (nseg & 1) ^ 1, waits.limit));
             if (!ok) break;
             if (lane == 0) {
                 mbar_arrive_expect_tx(&q_full, (two ? 2 : 1) * TILE);
@@ -348,11 +356,12 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
                 const int y = a.page_shift > 7 ? (j * kKeys) & ((1 << a.page_shift) - 1) : 0;
 #pragma unroll
                 for (int kv = 0; kv < 2; ++kv) {
-                    ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[slot], empty_phase));
+                    ok = __all_sync(0xffffffffu, mbar_wait(&kv_empty[slot], empty_phase, waits.limit));
                     if (!ok) break;
-                    if (lane == 0) mbar_arrive_expect_tx(&kv_full[slot], TILE);
+                    const bool comes = cta != 0 || issued + 1 != waits.stalled;
+                    if (lane == 0 && comes) mbar_arrive_expect_tx(&kv_full[slot], TILE);
                     __syncwarp();
-                    if (lane < npg)
+                    if (lane < npg && comes)
                         for (int x = 0; x < NB; ++x)
                             tma_load_3d(ring + slot * TILE + x * kBox + lane * prow * 128, kv ? &mapV : &mapK, 64 * x, y, z,
                                         &kv_full[slot]);
@@ -390,11 +399,11 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
         };
         // what an early look at a barrier left open
         auto settle = [&](bool seen, uint64_t* bar, uint32_t parity) {
-            return __all_sync(0xffffffffu, seen) || warp_wait(bar, parity);
+            return __all_sync(0xffffffffu, seen) || warp_wait(bar, parity, waits.limit);
         };
         do {
             const int nt = two_halves(sg) ? 2 : 1;
-            ok = warp_wait(&q_full, nseg & 1) && warp_wait(&kv_full[slot], full_phase);
+            ok = warp_wait(&q_full, nseg & 1, waits.limit) && warp_wait(&kv_full[slot], full_phase, waits.limit);
             if (!ok) break;
             tc_fence_after();
             for (int t = 0; t < nt; ++t) scores(t, slot);
@@ -452,7 +461,7 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
         } while (ok && next_segment(sg, left));
         if (!ok && lane == 0) atomicExch(&s_fail, 1);
         warp_commit(&mdone);                         // every MMA has finished before TMEM is freed
-        if (!warp_wait(&mdone, 0) && lane == 0) atomicExch(&s_fail, 1);
+        if (!warp_wait(&mdone, 0, kWaitLimitNs) && lane == 0) atomicExch(&s_fail, 1);
     }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kRegsSoftmax));
@@ -488,8 +497,8 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
                 for (int i = 0; i < sg.len; ++i) {
                     const int key0 = (sg.c.j + i) * kKeys;
                     const bool masked = key0 + kKeys > lim0;
-                    bool ok = mbar_wait(&s_full[t], ph);
-                    if (t == 0 && masked) ok = ok && mbar_wait(&kv_full[vslot], v_phase);
+                    bool ok = mbar_wait(&s_full[t], ph, waits.limit);
+                    if (t == 0 && masked) ok = ok && mbar_wait(&kv_full[vslot], v_phase, waits.limit);
                     if (!__all_sync(0xffffffffu, ok)) { fail = true; break; }
                     tc_fence_after();
                     if (t == 0 && masked) {
@@ -584,7 +593,7 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
                     if (vslot >= nslots) { vslot -= nslots; v_phase ^= 1; }
                 }
                 // ---- end of the tile, or of this CTA's part of it: O holds every unit
-                if (!fail) fail = !mbar_wait(&o_full[t], ph ^ 1);
+                if (!fail) fail = !mbar_wait(&o_full[t], ph ^ 1, waits.limit);
                 stop = named_any(1 + t, 128, fail);
                 if (stop) break;
                 tc_fence_after();
@@ -681,7 +690,7 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
         if (lane == 0) report_status(a.status, LLAMA_ERR_DEVICE_TIMEOUT);
         // the newest copy of each slot and the last Q land before the CTA exits
         for (int k = issued > nslots ? issued - nslots : 0; k < issued; ++k)
-            mbar_wait(&kv_full[k % nslots], (k / nslots) & 1);
+            if (cta != 0 || k + 1 != waits.stalled) mbar_wait(&kv_full[k % nslots], (k / nslots) & 1);
         if (n_q > 0) mbar_wait(&q_full, (n_q - 1) & 1);
     }
 }
@@ -690,6 +699,7 @@ paged_attn_tile_kernel(const __grid_constant__ CUtensorMap mapQ, const __grid_co
 
 namespace {
 std::atomic<PFN_cuTensorMapEncodeTiled_v12000> g_encode3{nullptr};
+std::atomic<uint64_t> g_stall{0};               // an armed stall: stage + 1 << 32 | wait limit in ns (below 2^32); 0: none
 
 // A 3-d map of 16-bit values, boxes of 64 x b1 x b2, 128-byte swizzle.
 int encode_3d(CUtensorMap* map, const void* base, int dtype, long long d0, long long d1, long long d2, long long s1,
@@ -755,12 +765,21 @@ static int tile_go(const PagedAttnArgs& a, int dtype, cudaStream_t st) {
     const long long cap = ((static_cast<long long>(a.max_pages) << a.page_shift) + kKeys - 1) / kKeys;
     long long grid = static_cast<long long>(a.T) * a.nkv * cap;
     if (grid > sms) grid = sms;
-    kern<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(mq, mk, mv, a, shape, nslots);
+    Waits waits = {kWaitLimitNs, 0};
+    if (g_stall.load(std::memory_order_relaxed)) {
+        const uint64_t s = g_stall.exchange(0);
+        if (s) waits = {s & 0xffffffffu, static_cast<int>(s >> 32)};
+    }
+    kern<<<static_cast<unsigned>(grid), kThreads, smem, st>>>(mq, mk, mv, a, shape, nslots, waits);
     LLB_CHECK_LAUNCH("paged_attn_tile_kernel");
     return LLAMA_OK;
 }
 
 size_t paged_attention_tile_ws(int hd) { return ws_bytes(hd); }
+
+void arm_paged_stall(int stage, long long wait_ns) {
+    g_stall.store(stage < 0 ? 0 : (static_cast<uint64_t>(stage) + 1) << 32 | static_cast<uint64_t>(wait_ns));
+}
 
 int launch_paged_attention_tile(const PagedAttnArgs& a, int dtype, cudaStream_t st) {
     if (dtype == LLAMA_F16) return a.hd == 64 ? tile_go<f16, 64>(a, dtype, st) : tile_go<f16, 128>(a, dtype, st);

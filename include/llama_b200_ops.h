@@ -224,10 +224,15 @@ LLAMA_API int llama_timeline_stop(llama_model* m, uint64_t* end_ns, int32_t* kin
  * (1 us .. 2 s).  A unit past the end of CTA 0's run stalls nothing.  The
  * outputs of that step are unspecified; llama_model_status then returns the
  * timeout code and resets the model's internal counters, after which the next
- * call computes correctly.  LLAMA_STALL_NONE disarms a stall not yet taken. */
+ * call computes correctly.  LLAMA_STALL_NONE disarms a stall not yet taken.
+ * Without a model (m NULL), LLAMA_STALL_PAGED arms the next llama_paged_attention
+ * call of this process that takes the chunk kernel: stage 2i is the K tile of
+ * CTA 0's i-th unit, 2i + 1 its V tile; the code arrives in that call's status,
+ * and its workspace is zeroed before the next call. */
 #define LLAMA_STALL_NONE        0
 #define LLAMA_STALL_PROJECTION  1
 #define LLAMA_STALL_ATTENTION   2
+#define LLAMA_STALL_PAGED       3
 LLAMA_API int llama_debug_stall(llama_model* m, int which, int unit, int64_t wait_limit_ns);
 
 #ifdef __cplusplus
