@@ -769,9 +769,11 @@ def paged_attention(q, k_pages, v_pages, block_tables, cu_new, seq_lens, out, ma
                     scale: Optional[float] = None, workspace=None, status=None, stream=None):
     """Causal attention of each request's new tokens (packed rows cu_new[b] ..
     of q [T, n_heads, head_dim]) over its pages (llama_paged_attention).
-    max_new: most new tokens of one request (None: T); scale: 1/sqrt(head_dim)
-    if None.  workspace: paged_attention_workspace(), kept by the caller; None
-    makes a new one for this call."""
+    max_new: most new tokens of one request; None takes T, the most that there
+    can be, so pass it where requests are many: single tokens are slower on the
+    chunk kernel that a high max_new chooses.  scale: 1/sqrt(head_dim) if None.
+    workspace: paged_attention_workspace(), kept by the caller; None makes and
+    zeroes a new one (up to 42 MB) for this call."""
     torch = _torch()
     dev = _home(q, "q")
     dt, i32 = q.dtype, torch.int32

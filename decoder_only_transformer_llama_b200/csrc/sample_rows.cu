@@ -16,7 +16,7 @@
 // weigh nothing.
 //
 // Measured: 1 x 32000 logits 11 us (six exchanges over the cluster, latency), 64 x 128000
-// with parameters of every kind 62 us (rows with top-k 34, with min-p 40, with top-p 75; of
+// with parameters of every kind 63 us (rows with top-k 34, with min-p 40, with top-p 75; of
 // the histogram pass of the latter, 14 us, the additions to shared memory take 8, whose
 // lanes meet in banks, and the exponentials 4), against 1.28 ms and 5.2 ms of one CTA per row
 // with a radix select over whole-row passes.

@@ -200,7 +200,9 @@ LLAMA_API int llama_decode_step(llama_model* m, const int32_t* tokens, int32_t* 
  * softmax(logits / temperature); tokens ordered by p descending (ties by id
  * ascending); token k kept iff the mass before it <= top_p; returns the first
  * kept token whose cumulative mass exceeds uniforms[b] * (kept mass), or the
- * last kept token.  Needs no model and no workspace. */
+ * last kept token.  Masses are exponentials relative to the largest, rounded to
+ * 2^-46 (2^-45 for V = 262144, where 2^-46 would not fit the sum's 64 bits).
+ * Needs no model and no workspace. */
 LLAMA_API int llama_sample(const float* logits, int B, int V, float temperature, float top_p,
                  const float* uniforms, int32_t* out, void* stream);
 
@@ -212,7 +214,7 @@ LLAMA_API int llama_sample(const float* logits, int B, int V, float temperature,
  *   min_p        device fp32 [B] or NULL, in [0, 1]; 0 keeps every token
  *   uniforms     device fp32 [B] in [0, 1) (clamped to it; read for every row)
  *   out          device int32 [B]
- * In fp64: e = exp((logit - max logit) / temperature); tokens ordered by logit
+ * With e = exp((logit - max logit) / temperature), tokens ordered by logit
  * descending, ties by id ascending.  Kept are the first top_k tokens; of them
  * those whose mass before them is <= top_p * (mass of the first top_k); of
  * those the ones with e >= min_p (the first token is always kept).  Returns
@@ -221,9 +223,13 @@ LLAMA_API int llama_sample(const float* logits, int B, int V, float temperature,
  * largest logit is +inf, the tokens at +inf share the mass equally.  A row
  * without any logit above -inf gives token 0.  A row whose temperature is
  * negative, NaN or above 1e30, whose top_p is negative or NaN, or whose min_p
- * is outside [0, 1] or NaN gives -1.  With top_k and min_p off the picks on
- * finite logits are those of llama_sample.  Needs no model and
- * no workspace.  LLAMA_ERR_INVALID_ARG for NULL pointers and sizes out of
+ * is outside [0, 1] or NaN gives -1.  Masses e are computed in fp64 (a table and
+ * a polynomial, within 2^-48) and rounded to 2^-46 of the largest (2^-45 for V =
+ * 262144); their sums are exact.  So a token below half a unit is never drawn,
+ * and a uniform, top_p or min_p that lies within the rounding of a border may
+ * fall to its other side.  With top_k and min_p off the rule on finite logits is
+ * that of llama_sample, whose exponentials are exp's: the picks are the same but
+ * for such borders.  Needs no model and no workspace.  LLAMA_ERR_INVALID_ARG for NULL pointers and sizes out of
  * range; B == 0 is a no-op. */
 LLAMA_API int llama_sample_rows(const float* logits, int B, int V, const float* temperature, const int32_t* top_k,
                                 const float* top_p, const float* min_p, const float* uniforms, int32_t* out,

@@ -140,12 +140,18 @@ LLAMA_API int llama_paged_append(const void* q, int64_t q_stride, const void* k,
                                  void* v_pages, int n_pages, int page_size, int dtype, int32_t* status, void* stream);
 
 /* Causal grouped-query attention of each request's new tokens over its pages.
- *   q, out      [T, n_heads, head_dim] in the cache's dtype (fp32 sums)
+ *   q, out      [T, n_heads, head_dim] in the cache's dtype.  Scores, softmax
+ *               statistics and sums are fp32; with a 16-bit cache the weights
+ *               exp(score - maximum) are rounded once to its type for the
+ *               product with V (their sum is taken before), as in the model's
+ *               own attention, and the output is rounded once
  *   seq_lens    int32 [B]: tokens of each request in the cache, the new ones
  *               included: row i of request b's n new tokens sits at position
  *               seq_lens[b] - n + i and sees keys 0 .. that position
  *   max_new     most new tokens of one request (host): it chooses the kernel
- *               and sizes the workspace; a request with more is still right
+ *               and sizes the workspace; a request with more is still right,
+ *               but one far too high gives single tokens the chunk kernel's
+ *               256-row tiles
  *   scale       factor of the scores (1/sqrt(head_dim) for the model's attention)
  *   workspace   llama_paged_attention_workspace_bytes() of device scratch,
  *               256-byte aligned, zero-filled before its first use (the kernels
