@@ -8,9 +8,6 @@
 #include <cuda.h>
 #include <stdint.h>
 
-#include <atomic>
-#include <mutex>
-
 #include "../../include/llama_b200.h"
 
 namespace llb {
@@ -29,37 +26,6 @@ int cuda_fail(cudaError_t e, const char* what);
         cudaError_t _e = cudaGetLastError();                    \
         if (_e != cudaSuccess) return ::llb::cuda_fail(_e, what); \
     } while (0)
-
-// What a launcher asks of the device or sets on it once: a kernel's attributes
-// hold on the device they were set on.  Any host thread may be the first.
-template <typename V>
-class PerDevice {
-  public:
-    // *out = the current device's value, filled by make(device, out) on the first call there.
-    template <typename F>
-    cudaError_t get(V* out, F make) {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        if (dev < 0 || dev >= kDevices) return make(dev, out);
-        if (!ready_[dev].load(std::memory_order_acquire)) {
-            std::lock_guard<std::mutex> lock(mu_);
-            if (!ready_[dev].load(std::memory_order_relaxed)) {
-                e = make(dev, &value_[dev]);
-                if (e != cudaSuccess) return e;
-                ready_[dev].store(true, std::memory_order_release);
-            }
-        }
-        *out = value_[dev];
-        return cudaSuccess;
-    }
-
-  private:
-    static constexpr int kDevices = 64;
-    std::mutex mu_;
-    std::atomic<bool> ready_[kDevices] = {};
-    V value_[kDevices] = {};
-};
 
 // ---------------------------------------------------------------- device status
 // One int per model: the first device-detected error code wins.

@@ -34,6 +34,7 @@
 #include "common.cuh"
 #include "paged.h"
 #include "paged_work.cuh"
+#include "per_device.cuh"
 
 namespace llb {
 

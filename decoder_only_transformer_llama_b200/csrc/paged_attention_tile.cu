@@ -36,11 +36,13 @@
 // sub-tile by the last to arrive, in CTA order.
 #include <cudaTypedefs.h>
 
+#include <atomic>
 #include <type_traits>
 
 #include "common.cuh"
 #include "paged.h"
 #include "paged_work.cuh"
+#include "per_device.cuh"
 
 namespace llb {
 

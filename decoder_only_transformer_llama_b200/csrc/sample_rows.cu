@@ -33,6 +33,7 @@
 // by histograms over the order key, 10 bits of it at a time.
 #include "common.cuh"
 #include "paged.h"
+#include "per_device.cuh"
 #include "sample_mass.cuh"
 
 namespace llb {
